@@ -9,17 +9,21 @@ path. Calling any function without the built library, or with CPU tensors, raise
 Functions mirror the C entry points:
     fwd(q, k, v, log_g, beta, h0=None, cu_seqlens=None, ...)  -> (o, hT)     [kda_fwd]
     decode_step(q, k, v, log_g, beta, S, o=None)               -> o          [kda_decode_step]
+    linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, ...)  -> (o, hT)     [kda_linear_fwd]
+    linear_decode(q, k, v, log_g, S, o=None)                   -> o          [kda_linear_decode]
     get_device_error(stream=None)                                             [kda_get_device_error]
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 
 import torch
 
 __all__ = ["fwd", "fwd_no_alloc", "out_norm_gated", "short_conv", "decode_step", "decode_tokens",
+           "linear_fwd", "linear_decode", "linear_fwd_workspace_size",
            "get_device_error",
            "fwd_workspace_size",
            "fwd_workspace_size_min", "fwd_algorithm",
@@ -32,7 +36,8 @@ _LIB_PATH = _PKG / "libkda.so"
 CHUNK_AUTO, CHUNK_PER_TOKEN, CHUNK_64 = 0, 1, 64
 KDA_F32, KDA_BF16 = 0, 1
 STATUS = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED", 3: "KDA_ERR_CUDA",
-          4: "KDA_ERR_TIMEOUT", 5: "KDA_ERR_BAD_SEQLENS", 6: "KDA_ERR_RANGE"}
+          4: "KDA_ERR_TIMEOUT", 5: "KDA_ERR_BAD_SEQLENS", 6: "KDA_ERR_RANGE",
+          7: "KDA_ERR_BAD_INDEX"}
 
 
 class KdaError(RuntimeError):
@@ -46,6 +51,12 @@ class FwdDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("num_seqs", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("chunk_size", ctypes.c_int)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+                ("num_seqs", ctypes.c_int), ("dtype", ctypes.c_int), ("gate", ctypes.c_int)]
 
 
 class OutNorm(ctypes.Structure):
@@ -99,6 +110,12 @@ def lib():
     L.kda_decode_step.restype = i32
     L.kda_decode_tokens.argtypes = [i32, i32, i32, i32, i32, i32, p, p, p, p, p, p, p, p]
     L.kda_decode_tokens.restype = i32
+    L.kda_linear_fwd.argtypes = [ctypes.POINTER(LinearDesc)] + [p] * 9 + [sz, p]
+    L.kda_linear_fwd.restype = i32
+    L.kda_linear_fwd_workspace_size.argtypes = [ctypes.POINTER(LinearDesc)]
+    L.kda_linear_fwd_workspace_size.restype = sz
+    L.kda_linear_decode.argtypes = [i32] * 8 + [p] * 7
+    L.kda_linear_decode.restype = i32
     L.kda_get_device_error.argtypes = [p]
     L.kda_get_device_error.restype = i32
     L.kda_status_string.argtypes = [i32]
@@ -521,6 +538,124 @@ def decode_tokens(q, k, v, log_g, beta, S, *, o=None, stream=None):
                                      _ptr(log_g), _ptr(beta), _ptr(S), _ptr(o),
                                      _stream(stream, dev))
     _check(st, "kda_decode_tokens")
+    return o
+
+
+def _on(stream):
+    """Allocate for work on `stream`: a tensor made here comes from that stream's memory, so that
+    nothing pending on the current stream still uses it and its reuse follows the call."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+GATE_TOKEN, GATE_HEAD = 0, 1
+
+
+def _linear_gate(log_g, shape, device):
+    """Gate kind of log_g: [H] (one decay for each head) or one per token and head."""
+    one = isinstance(log_g, torch.Tensor) and log_g.dim() == 1
+    _dev(log_g, "log_g", torch.float32, shape[-1:] if one else shape, device)
+    return GATE_HEAD if one else GATE_TOKEN
+
+
+def linear_fwd_workspace_size(B, T, H, Hk, dk, dv, num_seqs, dtype=torch.bfloat16,
+                              gate=GATE_TOKEN) -> int:
+    d = LinearDesc(B, T, H, Hk, dk, dv, num_seqs,
+                   KDA_BF16 if dtype == torch.bfloat16 else KDA_F32, gate)
+    return int(lib().kda_linear_fwd_workspace_size(ctypes.byref(d)))
+
+
+def linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, *, output_final_state: bool = True,
+               o=None, hT=None, workspace=None, stream=None):
+    """Prefill of linear attention with a scalar decay for each head (``kda_linear_fwd``):
+    S = exp(log_g) S + k v^T, o = S^T q.
+
+    q, k: [B, T, Hk, dk]; v: [B, T, H, dv], H a multiple of Hk (value head h reads q, k head
+    h // (H / Hk)); q/k/v share one dtype (bf16 or fp32). log_g: fp32 [B, T, H], or [H] for one
+    decay per head. h0: [N, H, dk, dv] fp32 or None. cu_seqlens: int32 [N + 1] on the device (B
+    must be 1) or None. Returns (o [B, T, H, dv], hT [N, H, dk, dv] fp32 or None). hT must not
+    overlap h0, nor o any input. The workspace (uint8, linear_fwd_workspace_size bytes) is
+    allocated here when not given; calls that may overlap need one each.
+    """
+    lib()
+    _dev(q, "q")
+    dev = q.device
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hk, dk]")
+    B, T, Hk, dk = q.shape
+    dt = q.dtype
+    _dtype_code(q)
+    _dev(k, "k", dt, (B, T, Hk, dk), dev)
+    _dev(v, "v", dt, None, dev)
+    if v.dim() != 4 or tuple(v.shape[:2]) != (B, T):
+        raise ValueError("v must be [B, T, H, dv]")
+    H, dv = v.shape[2:]
+    gate = _linear_gate(log_g, (B, T, H), dev)
+    N = B
+    if cu_seqlens is not None:
+        _dev(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a 1-D int32 tensor of N + 1 offsets")
+        N = cu_seqlens.numel() - 1
+    _dev(h0, "h0", torch.float32, (N, H, dk, dv), dev)
+    if o is None:
+        with _on(stream):
+            o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+    else:
+        _dev(o, "o", dt, (B, T, H, dv), dev)
+    if not output_final_state:
+        hT = None
+    elif hT is None:
+        with _on(stream):
+            hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    else:
+        _dev(hT, "hT", torch.float32, (N, H, dk, dv), dev)
+    desc = LinearDesc(B, T, H, Hk, dk, dv, N, _dtype_code(q), gate)
+    if workspace is None:
+        need = int(lib().kda_linear_fwd_workspace_size(ctypes.byref(desc)))
+        if need > 0:
+            with _on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _dev(workspace, "workspace", torch.uint8, None, dev)
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    with torch.cuda.device(dev):
+        st = lib().kda_linear_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_g),
+                                  _ptr(h0), _ptr(cu_seqlens), _ptr(o), _ptr(hT), _ptr(workspace),
+                                  ws_bytes, _stream(stream, dev))
+    _check(st, "kda_linear_fwd")
+    return o, hT
+
+
+def linear_decode(q, k, v, log_g, S, *, o=None, stream=None):
+    """One token (q, k: [N, Hk, dk], v: [N, H, dv]) or T tokens ([N, T, ...]) of linear attention
+    for N sequences (``kda_linear_decode``); S [N, H, dk, dv] fp32 is updated in place. log_g: fp32
+    [N, H] or [N, T, H] to match, or [H] for one decay per head. Returns o like v."""
+    lib()
+    _dev(q, "q")
+    dev = q.device
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [N, Hk, dk] or [N, T, Hk, dk]")
+    lead = tuple(q.shape[:-2])
+    N, T = lead[0], lead[1] if len(lead) == 2 else 1
+    Hk, dk = q.shape[-2:]
+    dt = q.dtype
+    _dtype_code(q)
+    _dev(k, "k", dt, tuple(q.shape), dev)
+    _dev(v, "v", dt, None, dev)
+    if v.dim() != q.dim() or tuple(v.shape[:-2]) != lead:
+        raise ValueError("v must be %s" % ("[N, H, dv]" if len(lead) == 1 else "[N, T, H, dv]"))
+    H, dv = v.shape[-2:]
+    gate = _linear_gate(log_g, (*lead, H), dev)
+    _dev(S, "S", torch.float32, (N, H, dk, dv), dev)
+    if o is None:
+        with _on(stream):
+            o = torch.empty(tuple(v.shape), dtype=dt, device=dev)
+    else:
+        _dev(o, "o", dt, tuple(v.shape), dev)
+    with torch.cuda.device(dev):
+        st = lib().kda_linear_decode(N, T, H, Hk, dk, dv, _dtype_code(q), gate, _ptr(q), _ptr(k),
+                                     _ptr(v), _ptr(log_g), _ptr(S), _ptr(o), _stream(stream, dev))
+    _check(st, "kda_linear_decode")
     return o
 
 

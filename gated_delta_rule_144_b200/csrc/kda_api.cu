@@ -13,6 +13,7 @@
 
 #include "kda_bwd.cuh"
 #include "kda_internal.cuh"
+#include "kda_linear.cuh"
 #include "kda_scan.cuh"
 
 namespace {
@@ -134,6 +135,7 @@ const char* kda_status_string(kda_status_t s) {
         case KDA_ERR_TIMEOUT: return "device pipeline wait timed out";
         case KDA_ERR_BAD_SEQLENS: return "malformed cu_seqlens";
         case KDA_ERR_RANGE: return "decay out of range (reserved; no longer raised)";
+        case KDA_ERR_BAD_INDEX: return "tree parent, path row or state page out of range";
     }
     return "unknown status";
 }
@@ -750,6 +752,165 @@ kda_status_t kda_decode_tokens(int N, int H, int T, int dk, int dv, kda_dtype_t 
     }
     if (e != cudaSuccess) return cuda_fail(e, "kda_decode_tokens launch");
     return KDA_OK;
+}
+
+// ------------------------------------------------------------------ linear attention
+
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+static kda_status_t check_linear_desc(const kda_linear_desc_t* d, bool has_cu) {
+    if (!d) return fail(KDA_ERR_INVALID_ARG, "desc is NULL");
+    if (d->B < 1 || d->T < 0 || d->H < 1 || d->Hk < 1 || d->dk < 1 || d->dv < 1 || d->num_seqs < 0)
+        return fail(KDA_ERR_INVALID_ARG, "bad sizes B=%d T=%d H=%d Hk=%d dk=%d dv=%d N=%d", d->B,
+                    d->T, d->H, d->Hk, d->dk, d->dv, d->num_seqs);
+    if (d->H % d->Hk)
+        return fail(KDA_ERR_INVALID_ARG, "H = %d is not a multiple of Hk = %d", d->H, d->Hk);
+    if (d->dtype != KDA_F32 && d->dtype != KDA_BF16)
+        return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)d->dtype);
+    if (d->gate != KDA_GATE_TOKEN && d->gate != KDA_GATE_HEAD)
+        return fail(KDA_ERR_INVALID_ARG, "unknown gate %d", (int)d->gate);
+    if (d->dk > 256 || d->dv > 256)
+        return fail(KDA_ERR_UNSUPPORTED, "linear attention supports dk, dv <= 256");
+    if (has_cu) {
+        if (d->B != 1) return fail(KDA_ERR_INVALID_ARG, "cu_seqlens requires B == 1");
+        if (d->num_seqs == 0 && d->T > 0)
+            return fail(KDA_ERR_INVALID_ARG, "%d tokens but no documents", d->T);
+    } else if (d->num_seqs != d->B) {
+        return fail(KDA_ERR_INVALID_ARG, "num_seqs (%d) must equal B (%d) without cu_seqlens",
+                    d->num_seqs, d->B);
+    }
+    if ((int64_t)d->B * d->T * d->H > (int64_t)1 << 40 || (int64_t)d->B * d->T > 0x7fffffffLL ||
+        (int64_t)d->num_seqs * d->H > 0x7fffffffLL)
+        return fail(KDA_ERR_INVALID_ARG, "problem too large");
+    return KDA_OK;
+}
+
+// Tokens per segment of the per-token walk (0: whole sequences). The walk has one warp per 8 value
+// columns of a (segment, head); segments are cut so that about 4096 warps (7 per scheduler) share
+// the work, and are not worth their states below 64 tokens.
+static int linear_segment(const kda_linear_desc_t* d) {
+    const int64_t groups = (int64_t)d->H * ((d->dv + 7) / 8);
+    const int64_t want = ((int64_t)d->B * d->T * groups / 4096 + 31) / 32 * 32;
+    const int L = (int)std::max<int64_t>(64, want);
+    if (d->num_seqs * groups >= 4096 || d->num_seqs > 1024 || d->H > 65535) return 0;
+    return d->T > L ? L : 0;
+}
+
+struct LinearLayout {
+    int seg_tokens, slots;
+    size_t decay, total;
+};
+
+static LinearLayout linear_layout(const kda_linear_desc_t* d, bool packed) {
+    LinearLayout L{linear_segment(d), d->num_seqs, 0, 0};
+    if (L.seg_tokens == 0) return L;
+    const int segs = (d->T + L.seg_tokens - 1) / L.seg_tokens;
+    L.slots = packed ? d->T / L.seg_tokens + d->num_seqs : d->num_seqs * segs;
+    L.decay = up256((size_t)L.slots * d->H * d->dk * d->dv * sizeof(float));
+    L.total = L.decay + up256((size_t)L.slots * d->H * sizeof(float));
+    return L;
+}
+
+size_t kda_linear_fwd_workspace_size(const kda_linear_desc_t* desc) {
+    if (check_linear_desc(desc, desc && desc->B == 1) != KDA_OK) return 0;
+    t_last_error[0] = 0;
+    // B == 1 may come with cu_seqlens, whose numbering needs one slot more per document
+    return linear_layout(desc, desc->B == 1).total;
+}
+
+static kda::LinearParams linear_params(const kda_linear_desc_t* d) {
+    kda::LinearParams p{};
+    p.B = d->B; p.T = d->T; p.H = d->H; p.Hk = d->Hk; p.dk = d->dk; p.dv = d->dv;
+    p.N = d->num_seqs;
+    p.bf16 = d->dtype == KDA_BF16;
+    p.gate_head = d->gate == KDA_GATE_HEAD;
+    p.slots = d->num_seqs;
+    return p;
+}
+
+kda_status_t kda_linear_fwd(const kda_linear_desc_t* d, const void* q, const void* k,
+                            const void* v, const float* log_g, const float* h0,
+                            const int32_t* cu_seqlens, void* o, float* hT, void* workspace,
+                            size_t workspace_bytes, kda_stream_t stream) {
+    t_last_error[0] = 0;
+    kda_status_t st = check_linear_desc(d, cu_seqlens != nullptr);
+    if (st != KDA_OK) return st;
+    const bool tokens = (int64_t)d->B * d->T > 0;
+    if ((st = check_ptr(q, "q", tokens)) || (st = check_ptr(k, "k", tokens)) ||
+        (st = check_ptr(v, "v", tokens)) || (st = check_ptr(log_g, "log_g", tokens)) ||
+        (st = check_ptr(h0, "h0", false)) || (st = check_ptr(hT, "hT", false)) ||
+        (st = check_ptr(o, "o", tokens)) || (st = check_ptr(cu_seqlens, "cu_seqlens", false)))
+        return st;
+    const size_t esz = d->dtype == KDA_BF16 ? 2 : 4, rows = (size_t)d->B * d->T;
+    const size_t qk_bytes = rows * d->Hk * d->dk * esz, v_bytes = rows * d->H * d->dv * esz;
+    const size_t h_bytes = (size_t)d->num_seqs * d->H * d->dk * d->dv * sizeof(float);
+    if (overlap(o, v_bytes, q, qk_bytes) || overlap(o, v_bytes, k, qk_bytes) ||
+        overlap(o, v_bytes, v, v_bytes))
+        return fail(KDA_ERR_INVALID_ARG, "o overlaps q, k or v");
+    if (overlap(hT, h_bytes, h0, h_bytes)) return fail(KDA_ERR_INVALID_ARG, "hT overlaps h0");
+    const LinearLayout L = linear_layout(d, cu_seqlens != nullptr);
+    if (L.total > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < L.total))
+        return fail(KDA_ERR_INVALID_ARG,
+                    "workspace must be a 16-byte aligned device buffer of %zu bytes "
+                    "(kda_linear_fwd_workspace_size)", L.total);
+    if (d->num_seqs == 0) return KDA_OK;
+    kda::LinearParams p = linear_params(d);
+    p.q = q; p.k = k; p.v = v; p.log_g = log_g; p.h0 = h0; p.cu_seqlens = cu_seqlens;
+    p.o = o; p.hT = hT;
+    if ((st = device_error_word(&p.err)) != KDA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (L.seg_tokens == 0) {
+        e = kda::launch_linear_walk(p, kda::LinearPass::kWhole, s);
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_linear_fwd launch");
+    }
+    p.seg_tokens = L.seg_tokens;
+    p.slots = L.slots;
+    p.seg_state = static_cast<float*>(workspace);
+    p.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.decay);
+    if (cu_seqlens && (e = kda::launch_linear_check(p, s)) != cudaSuccess)
+        return cuda_fail(e, "kda_linear_fwd cu_seqlens check");
+    if ((e = kda::launch_linear_walk(p, kda::LinearPass::kStates, s)) != cudaSuccess ||
+        (e = kda::launch_linear_combine(p, s)) != cudaSuccess ||
+        (e = kda::launch_linear_walk(p, kda::LinearPass::kOutputs, s)) != cudaSuccess)
+        return cuda_fail(e, "kda_linear_fwd launch");
+    return KDA_OK;
+}
+
+kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_dtype_t dtype,
+                               kda_gate_t gate, const void* q, const void* k, const void* v,
+                               const float* log_g, float* S_inout, void* o, kda_stream_t stream) {
+    t_last_error[0] = 0;
+    if (N < 0) return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%d", N);
+    // N sequences of T tokens; N = 0 is checked like N = 1
+    const kda_linear_desc_t d{std::max(N, 1), T, H, Hk, dk, dv, std::max(N, 1), dtype, gate};
+    kda_status_t st = check_linear_desc(&d, false);
+    if (st != KDA_OK) return st;
+    const bool any = N > 0 && T > 0;
+    if ((st = check_ptr(q, "q", any)) || (st = check_ptr(k, "k", any)) ||
+        (st = check_ptr(v, "v", any)) || (st = check_ptr(log_g, "log_g", any)) ||
+        (st = check_ptr(S_inout, "S_inout", any)) || (st = check_ptr(o, "o", any)))
+        return st;
+    if (!any) return KDA_OK;
+    const size_t esz = dtype == KDA_BF16 ? 2 : 4, rows = (size_t)N * T;
+    const size_t qk_bytes = rows * Hk * dk * esz, v_bytes = rows * H * dv * esz;
+    const size_t s_bytes = (size_t)N * H * dk * dv * sizeof(float);
+    if (overlap(o, v_bytes, q, qk_bytes) || overlap(o, v_bytes, k, qk_bytes) ||
+        overlap(o, v_bytes, v, v_bytes))
+        return fail(KDA_ERR_INVALID_ARG, "o overlaps q, k or v");
+    if (overlap(S_inout, s_bytes, q, qk_bytes) || overlap(S_inout, s_bytes, k, qk_bytes) ||
+        overlap(S_inout, s_bytes, v, v_bytes) || overlap(S_inout, s_bytes, o, v_bytes))
+        return fail(KDA_ERR_INVALID_ARG, "S_inout overlaps another argument");
+    kda::LinearParams p = linear_params(&d);
+    p.q = q; p.k = k; p.v = v; p.log_g = log_g; p.o = o;
+    p.h0 = p.hT = S_inout;   // each warp reads its own block of S before it writes it
+    if ((st = device_error_word(&p.err)) != KDA_OK) return st;
+    const cudaError_t e = kda::launch_linear_walk(p, kda::LinearPass::kWhole,
+                                                  reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_linear_decode launch");
 }
 
 kda_status_t kda_get_device_error(kda_stream_t stream) {

@@ -54,7 +54,8 @@ typedef enum {
     KDA_ERR_CUDA = 3,         /* a CUDA runtime call failed; kda_last_error() has the text     */
     KDA_ERR_TIMEOUT = 4,      /* device: a bounded pipeline wait expired (kernel gave up)      */
     KDA_ERR_BAD_SEQLENS = 5,  /* device: cu_seqlens not non-decreasing from 0 to T             */
-    KDA_ERR_RANGE = 6         /* reserved: no longer raised (steep decays take a direct path)  */
+    KDA_ERR_RANGE = 6,        /* reserved: no longer raised (steep decays take a direct path)  */
+    KDA_ERR_BAD_INDEX = 7     /* device: a tree parent, path row or state page out of range    */
 } kda_status_t;
 
 typedef enum {
@@ -338,8 +339,59 @@ kda_status_t kda_decode_tokens(int N, int H, int T, int dk, int dv, kda_dtype_t 
                                const void* beta, float* S_inout, void* o, kda_stream_t stream);
 
 /*
+ * Linear attention with a scalar decay for each head: the same kind of state without the delta
+ * rule and with one gate per (token, head), or one per head. Per (sequence, head), in order,
+ *
+ *     S = exp(log_g_t) S + k_t v_t^T,     o_t = S^T q_t       (read-out after the write; no scale)
+ *
+ *   B, T, H, dk, dv : batch, tokens per row, value heads, key and value head dims (dk, dv <= 256).
+ *   Hk              : query/key heads; H % Hk == 0 and value head h reads q, k head h / (H / Hk).
+ *   num_seqs, dtype : as in kda_fwd_desc_t (dtype: q, k, v and o).
+ *   gate            : KDA_GATE_TOKEN: log_g is [B, T, H]; KDA_GATE_HEAD: log_g is [H], one decay
+ *                     for every token. log_g is float32 and <= 0; -inf clears the state.
+ */
+typedef enum { KDA_GATE_TOKEN = 0, KDA_GATE_HEAD = 1 } kda_gate_t;
+typedef struct {
+    int B, T, H, Hk, dk, dv;
+    int num_seqs;
+    kda_dtype_t dtype;
+    kda_gate_t gate;
+} kda_linear_desc_t;
+
+/*
+ * kda_linear_fwd - prefill of the linear attention above over whole sequences or packed documents.
+ *
+ *   q, k : [B, T, Hk, dk] dtype      v, o : [B, T, H, dv] dtype      log_g : see gate
+ *   h0   : [N, H, dk, dv] float32 or NULL (zero)
+ *   hT   : [N, H, dk, dv] float32 or NULL; must not overlap h0. o must not overlap q, k or v.
+ *   cu_seqlens : as for kda_fwd (B = 1; empty documents keep their initial state).
+ *   workspace  : kda_linear_fwd_workspace_size(desc) bytes, 16-byte aligned (NULL when 0): the
+ *                states between the segments that long sequences are cut into, and their decays.
+ * Tokens of one document never reach another's outputs, whatever values they hold.
+ */
+kda_status_t kda_linear_fwd(const kda_linear_desc_t* desc, const void* q, const void* k,
+                            const void* v, const float* log_g, const float* h0,
+                            const int32_t* cu_seqlens, void* o, float* hT, void* workspace,
+                            size_t workspace_bytes, kda_stream_t stream);
+
+/* Workspace bytes kda_linear_fwd needs for `desc`. Host-only; 0 for a rejected description. */
+size_t kda_linear_fwd_workspace_size(const kda_linear_desc_t* desc);
+
+/*
+ * kda_linear_decode - advance N sequences by T tokens each (T = 1: one decode step), updating the
+ * state in place.
+ *   q, k : [N, T, Hk, dk] dtype      v, o : [N, T, H, dv] dtype
+ *   log_g : [N, T, H] (KDA_GATE_TOKEN) or [H] (KDA_GATE_HEAD), float32
+ *   S_inout : [N, H, dk, dv] float32; must not overlap any other argument.
+ * T = 0 or N = 0 does nothing.
+ */
+kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_dtype_t dtype,
+                               kda_gate_t gate, const void* q, const void* k, const void* v,
+                               const float* log_g, float* S_inout, void* o, kda_stream_t stream);
+
+/*
  * kda_get_device_error - synchronise `stream`, then return and clear the sticky device error
- * word (KDA_OK, KDA_ERR_BAD_SEQLENS or KDA_ERR_TIMEOUT), or KDA_ERR_CUDA if
+ * word (KDA_OK, KDA_ERR_BAD_SEQLENS, KDA_ERR_BAD_INDEX or KDA_ERR_TIMEOUT), or KDA_ERR_CUDA if
  * the synchronisation itself failed. The word is per device and shared by all streams.
  */
 kda_status_t kda_get_device_error(kda_stream_t stream);
