@@ -11,6 +11,9 @@ Functions mirror the C entry points:
     decode_step(q, k, v, log_g, beta, S, o=None)               -> o          [kda_decode_step]
     linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, ...)  -> (o, hT)     [kda_linear_fwd]
     linear_decode(q, k, v, log_g, S, o=None)                   -> o          [kda_linear_decode]
+    decode_tree(q, k, v, log_g, beta, parents, S, o=None)      -> o          [kda_decode_tree]
+    commit_path(k, v, log_g, beta, path, S)                                   [kda_commit_path]
+    state_copy(S, src, dst, page_dim=0)                                       [kda_state_copy]
     get_device_error(stream=None)                                             [kda_get_device_error]
 """
 
@@ -24,6 +27,7 @@ import torch
 
 __all__ = ["fwd", "fwd_no_alloc", "out_norm_gated", "short_conv", "decode_step", "decode_tokens",
            "linear_fwd", "linear_decode", "linear_fwd_workspace_size",
+           "decode_tree", "commit_path", "state_copy", "plan_compaction", "TREE_MAX_NODES",
            "get_device_error",
            "fwd_workspace_size",
            "fwd_workspace_size_min", "fwd_algorithm",
@@ -116,6 +120,12 @@ def lib():
     L.kda_linear_fwd_workspace_size.restype = sz
     L.kda_linear_decode.argtypes = [i32] * 8 + [p] * 7
     L.kda_linear_decode.restype = i32
+    L.kda_decode_tree.argtypes = [i32] * 4 + [p] * 9
+    L.kda_decode_tree.restype = i32
+    L.kda_commit_path.argtypes = [i32] * 5 + [p] * 7
+    L.kda_commit_path.restype = i32
+    L.kda_state_copy.argtypes = [p, i32, i32, ctypes.c_longlong, p, p, i32, p]
+    L.kda_state_copy.restype = i32
     L.kda_get_device_error.argtypes = [p]
     L.kda_get_device_error.restype = i32
     L.kda_status_string.argtypes = [i32]
@@ -657,6 +667,107 @@ def linear_decode(q, k, v, log_g, S, *, o=None, stream=None):
                                      _ptr(v), _ptr(log_g), _ptr(S), _ptr(o), _stream(stream, dev))
     _check(st, "kda_linear_decode")
     return o
+
+
+TREE_MAX_NODES = 64
+
+
+def _tree_rows(k, v, log_g, beta, S):
+    """(device, dtype, N, T, H) of [N, T, H, 128] rows and their states."""
+    _dev(k, "k")
+    dev, dt = k.device, k.dtype
+    if k.dim() != 4 or k.shape[3] != 128:
+        raise ValueError("k must be [N, T, H, 128]")
+    N, T, H, d = k.shape
+    _dtype_code(k)
+    _dev(v, "v", dt, (N, T, H, d), dev)
+    _dev(log_g, "log_g", torch.float32, (N, T, H, d), dev)
+    _dev(beta, "beta", dt, (N, T, H), dev)
+    _dev(S, "S", torch.float32, (N, H, d, d), dev)
+    return dev, dt, N, T, H
+
+
+def decode_tree(q, k, v, log_g, beta, parents, S, *, o=None, stream=None):
+    """Read-outs of every node of a tree of drafted tokens (``kda_decode_tree``) against the
+    states S [N, H, 128, 128] fp32, which stay as they are.
+
+    q, k, v: [N, T, H, 128] (bf16 or fp32), log_g: fp32 alike, beta: [N, T, H], T <= 64. parents:
+    int32 [N, T], -1 for a child of the committed state, else an earlier node, or -2 for no node:
+    o keeps that row (a new o holds zeros there). Returns o [N, T, H, 128]. Rejected parents leave
+    their sequence's rows and set KDA_ERR_BAD_INDEX (``get_device_error``).
+    """
+    lib()
+    dev, dt, N, T, H = _tree_rows(k, v, log_g, beta, S)
+    _dev(q, "q", dt, tuple(k.shape), dev)
+    _dev(parents, "parents", torch.int32, (N, T), dev)
+    if o is None:
+        with _on(stream):
+            o = torch.zeros(tuple(k.shape), dtype=dt, device=dev)
+    else:
+        _dev(o, "o", dt, tuple(k.shape), dev)
+    with torch.cuda.device(dev):
+        st = lib().kda_decode_tree(N, H, T, _dtype_code(k), _ptr(q), _ptr(k), _ptr(v),
+                                   _ptr(log_g), _ptr(beta), _ptr(parents), _ptr(S), _ptr(o),
+                                   _stream(stream, dev))
+    _check(st, "kda_decode_tree")
+    return o
+
+
+def commit_path(k, v, log_g, beta, path, S, *, stream=None):
+    """Advance the states S in place by the rows that path names (``kda_commit_path``): int32
+    [N, A], each row list ending at its first negative entry. Rows as for ``decode_tree``."""
+    lib()
+    dev, dt, N, T, H = _tree_rows(k, v, log_g, beta, S)
+    _dev(path, "path", torch.int32, None, dev)
+    if path.dim() != 2 or path.shape[0] != N:
+        raise ValueError("path must be [N, A]")
+    with torch.cuda.device(dev):
+        st = lib().kda_commit_path(N, H, T, path.shape[1], _dtype_code(k), _ptr(k), _ptr(v),
+                                   _ptr(log_g), _ptr(beta), _ptr(path), _ptr(S),
+                                   _stream(stream, dev))
+    _check(st, "kda_commit_path")
+
+
+def state_copy(S, src, dst, *, page_dim: int = 0, stream=None):
+    """Copy, fork or clear pages of a pool in place (``kda_state_copy``): along ``page_dim`` of S,
+    for every index of the dimensions before it (layers), page dst[i] takes page src[i], or zeros
+    where src[i] is -1; dst[i] = -1 does nothing. src, dst: int32 [n] on the device. S: any dtype,
+    contiguous, a page's bytes a multiple of 16. No page may be written twice, or both read and
+    written: such pairs, and ones out of range, are left out and set KDA_ERR_BAD_INDEX."""
+    lib()
+    _dev(S, "S")
+    dev = S.device
+    if not 0 <= page_dim < S.dim():
+        raise ValueError("page_dim must be a dimension of S")
+    _dev(src, "src", torch.int32, None, dev)
+    if src.dim() != 1:
+        raise ValueError("src must be 1-D")
+    _dev(dst, "dst", torch.int32, tuple(src.shape), dev)
+    layers = 1
+    for x in S.shape[:page_dim]:
+        layers *= x
+    page = S.element_size()
+    for x in S.shape[page_dim + 1:]:
+        page *= x
+    with torch.cuda.device(dev):
+        st = lib().kda_state_copy(_ptr(S), layers, S.shape[page_dim], page, _ptr(src), _ptr(dst),
+                                  src.numel(), _stream(stream, dev))
+    _check(st, "kda_state_copy")
+
+
+def plan_compaction(live):
+    """Moves that bring a pool's live pages to its front: live is a sequence of truth values, one
+    per page; returns (src, dst, where). Copying page src[i] to dst[i] leaves the live pages at
+    0 .. n - 1, where[p] is page p's new place (-1 for a dead one). Only pages behind n move, each
+    into a hole before n, lowest first, so no page is both read and written (host only)."""
+    live = [bool(x) for x in live]
+    n = sum(live)
+    dst = [p for p in range(n) if not live[p]]
+    src = [p for p in range(n, len(live)) if live[p]]
+    where = [p if a else -1 for p, a in enumerate(live)]
+    for a, b in zip(src, dst):
+        where[a] = b
+    return src, dst, where
 
 
 def get_device_error(stream=None, device=None) -> int:

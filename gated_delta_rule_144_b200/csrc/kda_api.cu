@@ -15,6 +15,7 @@
 #include "kda_internal.cuh"
 #include "kda_linear.cuh"
 #include "kda_scan.cuh"
+#include "kda_tree.cuh"
 
 namespace {
 
@@ -911,6 +912,98 @@ kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_
     const cudaError_t e = kda::launch_linear_walk(p, kda::LinearPass::kWhole,
                                                   reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_linear_decode launch");
+}
+
+// ------------------------------------------------------------------ trees of drafted tokens
+
+static kda_status_t check_tree_sizes(int N, int H, int T, kda_dtype_t dtype) {
+    if (N < 0 || H < 1 || T < 0)
+        return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%d H=%d T=%d", N, H, T);
+    if (dtype != KDA_F32 && dtype != KDA_BF16)
+        return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if ((int64_t)N * H > 0x7fffffffLL || (int64_t)N * T * H > (int64_t)1 << 40)
+        return fail(KDA_ERR_INVALID_ARG, "problem too large");
+    return KDA_OK;
+}
+
+kda_status_t kda_decode_tree(int N, int H, int T, kda_dtype_t dtype, const void* q, const void* k,
+                             const void* v, const float* log_g, const void* beta,
+                             const int32_t* parents, const float* S, void* o,
+                             kda_stream_t stream) {
+    t_last_error[0] = 0;
+    kda_status_t st = check_tree_sizes(N, H, T, dtype);
+    if (st != KDA_OK) return st;
+    if (T > KDA_TREE_MAX_NODES)
+        return fail(KDA_ERR_UNSUPPORTED, "%d nodes (at most %d)", T, KDA_TREE_MAX_NODES);
+    const bool any = N > 0 && T > 0;
+    if ((st = check_ptr(q, "q", any)) || (st = check_ptr(k, "k", any)) ||
+        (st = check_ptr(v, "v", any)) || (st = check_ptr(log_g, "log_g", any)) ||
+        (st = check_ptr(beta, "beta", any)) || (st = check_ptr(parents, "parents", any)) ||
+        (st = check_ptr(S, "S", any)) || (st = check_ptr(o, "o", any)))
+        return st;
+    if (!any) return KDA_OK;
+    const size_t rows = (size_t)N * T * H, x = rows * 128 * (dtype == KDA_BF16 ? 2 : 4);
+    if (overlap(o, x, q, x) || overlap(o, x, k, x) || overlap(o, x, v, x) ||
+        overlap(o, x, log_g, rows * 512) || overlap(o, x, beta, x / 128) ||
+        overlap(o, x, parents, (size_t)N * T * 4) || overlap(o, x, S, (size_t)N * H * 65536))
+        return fail(KDA_ERR_INVALID_ARG, "o overlaps another argument");
+    kda::TreeParams p{q, k, v, log_g, beta, parents, const_cast<float*>(S), o, N, H, T, 0,
+                      dtype == KDA_BF16, nullptr};
+    if ((st = device_error_word(&p.err)) != KDA_OK) return st;
+    const cudaError_t e = kda::launch_decode_tree(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_decode_tree launch");
+}
+
+kda_status_t kda_commit_path(int N, int H, int T, int A, kda_dtype_t dtype, const void* k,
+                             const void* v, const float* log_g, const void* beta,
+                             const int32_t* path, float* S_inout, kda_stream_t stream) {
+    t_last_error[0] = 0;
+    kda_status_t st = check_tree_sizes(N, H, T, dtype);
+    if (st != KDA_OK) return st;
+    if (A < 0) return fail(KDA_ERR_INVALID_ARG, "bad sizes A=%d", A);
+    const bool any = N > 0 && T > 0 && A > 0;
+    if ((st = check_ptr(k, "k", any)) || (st = check_ptr(v, "v", any)) ||
+        (st = check_ptr(log_g, "log_g", any)) || (st = check_ptr(beta, "beta", any)) ||
+        (st = check_ptr(path, "path", any)) || (st = check_ptr(S_inout, "S_inout", any)))
+        return st;
+    if (!any) return KDA_OK;
+    const size_t rows = (size_t)N * T * H, x = rows * 128 * (dtype == KDA_BF16 ? 2 : 4);
+    const size_t s = (size_t)N * H * 65536;
+    if (overlap(S_inout, s, k, x) || overlap(S_inout, s, v, x) ||
+        overlap(S_inout, s, log_g, rows * 512) || overlap(S_inout, s, beta, x / 128) ||
+        overlap(S_inout, s, path, (size_t)N * A * 4))
+        return fail(KDA_ERR_INVALID_ARG, "S_inout overlaps another argument");
+    kda::TreeParams p{nullptr, k, v, log_g, beta, path, S_inout, nullptr, N, H, T, A,
+                      dtype == KDA_BF16, nullptr};
+    if ((st = device_error_word(&p.err)) != KDA_OK) return st;
+    const cudaError_t e = kda::launch_commit_path(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_commit_path launch");
+}
+
+// ------------------------------------------------------------------ pages of states
+
+kda_status_t kda_state_copy(void* pool, int layers, int pages, long long page_bytes,
+                            const int32_t* src, const int32_t* dst, int n, kda_stream_t stream) {
+    t_last_error[0] = 0;
+    if (layers < 0 || pages < 0 || n < 0 || page_bytes < 1)
+        return fail(KDA_ERR_INVALID_ARG, "bad sizes layers=%d pages=%d page_bytes=%lld n=%d",
+                    layers, pages, page_bytes, n);
+    if (page_bytes % 16)
+        return fail(KDA_ERR_UNSUPPORTED, "page_bytes %lld is not a multiple of 16", page_bytes);
+    kda_status_t st;
+    const bool any = layers > 0 && n > 0;
+    if ((st = check_ptr(pool, "pool", any && pages > 0)) || (st = check_ptr(src, "src", any)) ||
+        (st = check_ptr(dst, "dst", any)))
+        return st;
+    if (!any) return KDA_OK;
+    const size_t bytes = (size_t)layers * pages * page_bytes, list = (size_t)n * 4;
+    if (overlap(pool, bytes, src, list) || overlap(pool, bytes, dst, list))
+        return fail(KDA_ERR_INVALID_ARG, "the pool overlaps src or dst");
+    unsigned* err = nullptr;
+    if ((st = device_error_word(&err)) != KDA_OK) return st;
+    const cudaError_t e = kda::launch_page_copy(pool, src, dst, n, layers, pages, page_bytes, err,
+                                                reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_state_copy launch");
 }
 
 kda_status_t kda_get_device_error(kda_stream_t stream) {

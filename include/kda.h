@@ -390,6 +390,53 @@ kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_
                                const float* log_g, float* S_inout, void* o, kda_stream_t stream);
 
 /*
+ * kda_decode_tree - the read-outs of every node of a tree of drafted tokens for N sequences, from
+ * their decode states, which stay as they are. Node i of sequence n has the state that the gated
+ * delta rule (see the head of this file) reaches from S[n] by the tokens on i's path from the
+ * root, i last; o[n, i] is that state's read-out with q[n, i].
+ *   q, k, log_g : [N, T, H, 128] (q, k in dtype, log_g float32)   v, o : [N, T, H, 128] dtype
+ *   beta        : [N, T, H] dtype
+ *   parents     : int32 [N, T], device: -1 for a child of the committed state, else an earlier
+ *                 node (0 <= parents[n, i] < i); -2 for no node (o keeps that row, and nothing of
+ *                 it is read but its gate and key rows, whose values do not matter).
+ *   S           : [N, H, 128, 128] float32.
+ * T <= KDA_TREE_MAX_NODES (KDA_ERR_UNSUPPORTED above). o must not overlap any other argument. A
+ * sequence with other parents gets no outputs and sets KDA_ERR_BAD_INDEX in the device error word.
+ * The states meet bf16 rows in tf32 products (relative error 2^-11 per factor, below the output's
+ * rounding), fp32 rows in split products (2^-21).
+ */
+#define KDA_TREE_MAX_NODES 64
+kda_status_t kda_decode_tree(int N, int H, int T, kda_dtype_t dtype, const void* q, const void* k,
+                             const void* v, const float* log_g, const void* beta,
+                             const int32_t* parents, const float* S, void* o, kda_stream_t stream);
+
+/*
+ * kda_commit_path - advance N sequences' states in place by the rows that a path names: what
+ * kda_decode_tokens does to the state for those rows in that order, without read-outs.
+ *   k, v, log_g, beta : [N, T, H, ...] as for kda_decode_tree
+ *   path    : int32 [N, A], device: rows (0 <= path < T) up to the first negative entry, which
+ *             ends the path. A row may be named more than once. An empty path leaves the state.
+ *   S_inout : [N, H, 128, 128] float32; must not overlap any other argument.
+ * A sequence whose path leaves the rows keeps its state and sets KDA_ERR_BAD_INDEX.
+ */
+kda_status_t kda_commit_path(int N, int H, int T, int A, kda_dtype_t dtype, const void* k,
+                             const void* v, const float* log_g, const void* beta,
+                             const int32_t* path, float* S_inout, kda_stream_t stream);
+
+/*
+ * kda_state_copy - copy, fork and clear pages of a pool of states in place: page dst[i] of every
+ * layer takes the contents of page src[i], or zeros where src[i] is -1. dst[i] = -1 does nothing
+ * (so a captured list can be shorter than its length).
+ *   pool     : [layers, pages, page_bytes], device; page_bytes a positive multiple of 16
+ *   src, dst : int32 [n], device
+ * The copies happen in no order: a page may be read by several pairs, but no page may be written
+ * twice, or both read and written. Pairs in such a conflict, or out of range, are left out and
+ * set KDA_ERR_BAD_INDEX in the device error word.
+ */
+kda_status_t kda_state_copy(void* pool, int layers, int pages, long long page_bytes,
+                            const int32_t* src, const int32_t* dst, int n, kda_stream_t stream);
+
+/*
  * kda_get_device_error - synchronise `stream`, then return and clear the sticky device error
  * word (KDA_OK, KDA_ERR_BAD_SEQLENS, KDA_ERR_BAD_INDEX or KDA_ERR_TIMEOUT), or KDA_ERR_CUDA if
  * the synchronisation itself failed. The word is per device and shared by all streams.
