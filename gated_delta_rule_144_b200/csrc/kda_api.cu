@@ -789,15 +789,50 @@ static kda_status_t check_linear_desc(const kda_linear_desc_t* d, bool has_cu) {
     return KDA_OK;
 }
 
+static bool linear_chunked(const kda_linear_desc_t* d) {
+    return kda::linear_chunk_takes(d->dtype == KDA_BF16, d->dk, d->dv);
+}
+
 // Tokens per segment of the per-token walk (0: whole sequences). The walk has one warp per 8 value
 // columns of a (segment, head); segments are cut so that about 4096 warps (7 per scheduler) share
 // the work, and are not worth their states below 64 tokens.
-static int linear_segment(const kda_linear_desc_t* d) {
+static int linear_walk_segment(const kda_linear_desc_t* d) {
     const int64_t groups = (int64_t)d->H * ((d->dv + 7) / 8);
     const int64_t want = ((int64_t)d->B * d->T * groups / 4096 + 31) / 32 * 32;
     const int L = (int)std::max<int64_t>(64, want);
-    if (d->num_seqs * groups >= 4096 || d->num_seqs > 1024 || d->H > 65535) return 0;
+    if (d->num_seqs * groups >= 4096) return 0;
     return d->T > L ? L : 0;
+}
+
+// Tokens per segment of the chunked kernel (0: whole sequences), whose CTAs take one (segment,
+// head, 64 value columns) each, one per SM. Equal lengths: the count of segments with the least
+// modelled time, in units of one chunk: waves of m chunks with outputs, and before them the
+// states of all segments but the last at half a chunk each, plus 2 units per CTA and 4 for the two
+// further launches. Packed documents, whose lengths the host does not see: segments of an SM's
+// even share of all chunks, at least 8.
+static int linear_chunk_segment(const kda_linear_desc_t* d, bool packed) {
+    const int n = (d->T + kda::kLinearChunk - 1) / kda::kLinearChunk;
+    const double units = (double)d->H * ((d->dv + 63) / 64), sms = 148.0;
+    if (packed) {
+        const int m = std::max(8, (int)std::ceil(n * units / sms));
+        return n > m ? m * kda::kLinearChunk : 0;
+    }
+    const double all = units * d->num_seqs;
+    double best = std::ceil(all / sms) * (n + 2.0);
+    int m_best = 0;
+    for (int m = 1; m < n; ++m) {
+        const int P = (n + m - 1) / m;
+        if (P > 64) continue;
+        const double cost = std::ceil(all * (P - 1) / sms) * (0.5 * m + 2.0) +
+                            std::ceil(all * P / sms) * (m + 2.0) + 4.0;
+        if (cost < best) best = cost, m_best = m;
+    }
+    return m_best * kda::kLinearChunk;
+}
+
+static int linear_segment(const kda_linear_desc_t* d, bool packed) {
+    if (d->num_seqs > 1024 || d->H > 65535) return 0;   // enough sequences to fill the GPU
+    return linear_chunked(d) ? linear_chunk_segment(d, packed) : linear_walk_segment(d);
 }
 
 struct LinearLayout {
@@ -806,7 +841,7 @@ struct LinearLayout {
 };
 
 static LinearLayout linear_layout(const kda_linear_desc_t* d, bool packed) {
-    LinearLayout L{linear_segment(d), d->num_seqs, 0, 0};
+    LinearLayout L{linear_segment(d, packed), d->num_seqs, 0, 0};
     if (L.seg_tokens == 0) return L;
     const int segs = (d->T + L.seg_tokens - 1) / L.seg_tokens;
     L.slots = packed ? d->T / L.seg_tokens + d->num_seqs : d->num_seqs * segs;
@@ -818,8 +853,9 @@ static LinearLayout linear_layout(const kda_linear_desc_t* d, bool packed) {
 size_t kda_linear_fwd_workspace_size(const kda_linear_desc_t* desc) {
     if (check_linear_desc(desc, desc && desc->B == 1) != KDA_OK) return 0;
     t_last_error[0] = 0;
-    // B == 1 may come with cu_seqlens, whose numbering needs one slot more per document
-    return linear_layout(desc, desc->B == 1).total;
+    // B == 1 may come with cu_seqlens, with other segments and one slot more per document
+    const size_t whole = desc->num_seqs == desc->B ? linear_layout(desc, false).total : 0;
+    return desc->B == 1 ? std::max(whole, linear_layout(desc, true).total) : whole;
 }
 
 static kda::LinearParams linear_params(const kda_linear_desc_t* d) {
@@ -864,8 +900,12 @@ kda_status_t kda_linear_fwd(const kda_linear_desc_t* d, const void* q, const voi
     if ((st = device_error_word(&p.err)) != KDA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
+    auto pass = [&](kda::LinearPass which) {
+        return linear_chunked(d) && tokens ? kda::launch_linear_chunk(p, which, s)
+                                           : kda::launch_linear_walk(p, which, s);
+    };
     if (L.seg_tokens == 0) {
-        e = kda::launch_linear_walk(p, kda::LinearPass::kWhole, s);
+        e = pass(kda::LinearPass::kWhole);
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_linear_fwd launch");
     }
     p.seg_tokens = L.seg_tokens;
@@ -874,9 +914,9 @@ kda_status_t kda_linear_fwd(const kda_linear_desc_t* d, const void* q, const voi
     p.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.decay);
     if (cu_seqlens && (e = kda::launch_linear_check(p, s)) != cudaSuccess)
         return cuda_fail(e, "kda_linear_fwd cu_seqlens check");
-    if ((e = kda::launch_linear_walk(p, kda::LinearPass::kStates, s)) != cudaSuccess ||
+    if ((e = pass(kda::LinearPass::kStates)) != cudaSuccess ||
         (e = kda::launch_linear_combine(p, s)) != cudaSuccess ||
-        (e = kda::launch_linear_walk(p, kda::LinearPass::kOutputs, s)) != cudaSuccess)
+        (e = pass(kda::LinearPass::kOutputs)) != cudaSuccess)
         return cuda_fail(e, "kda_linear_fwd launch");
     return KDA_OK;
 }

@@ -97,6 +97,10 @@ __device__ __forceinline__ bool linear_slot(const LinearParams& p, int g, Linear
 
 // CUDA-core walk, token by token in fp32: any dtype, dk, dv <= 256.
 cudaError_t launch_linear_walk(const LinearParams& p, LinearPass pass, cudaStream_t stream);
+// Chunks of 128 tokens on the tensor cores; seg_tokens a multiple of 128.
+constexpr int kLinearChunk = 128;
+bool linear_chunk_takes(bool bf16, int dk, int dv);
+cudaError_t launch_linear_chunk(const LinearParams& p, LinearPass pass, cudaStream_t stream);
 // Chains the segments' initial states: seg_state[n, s] <- state before segment s >= 1.
 cudaError_t launch_linear_combine(const LinearParams& p, cudaStream_t stream);
 // Sets the error word where cu_seqlens does not rise from 0 to T (segmented launches may not

@@ -235,3 +235,11 @@ def test_refusals():
     with pytest.raises(ValueError):
         kda.linear_decode(q[:, 0], k[:, 0], v, g, h0)
     assert kda.get_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 127, 128, 129, 1000, 9000])
+def test_long_prompt_single_head(T):
+    """Few chains: segments, and their states chained."""
+    x = make(1, T, 1, 1, 128, 64, seed=T, mu=-4.0)
+    o, hT = kda.linear_fwd(x["q"], x["k"], x["v"], x["log_g"], h0=x["h0"])
+    check(x, o, hT)
