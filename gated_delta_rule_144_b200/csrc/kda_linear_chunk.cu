@@ -11,29 +11,33 @@
 //
 // What keeps which precision.
 //   - The state stays fp32 in registers. What a chunk adds to it, K^T (decayed V), must not lose
-//     what fp32 holds, so the decayed v is split into three bf16 terms (8 bits each, 2^-25 left)
-//     and the three products are summed in fp32. The product runs once with N = 192, the three
-//     terms side by side.
+//     what fp32 holds, so the decayed v is split into three bf16 terms (8 bits each, 2^-25 left).
+//     The products of the first and of the two small terms are summed apart and meet in fp32.
 //   - q S reads the state rounded to bf16, and the decayed scores are rounded to bf16: each 2^-9
 //     of a term at most, as the output's own rounding, on disjoint parts of the output.
-//   - Decays are products of gates <= 1: a pair of rows in different 32-row blocks takes
+//   - Gate sums are held in powers of two. Decays are products of gates <= 1: a pair of rows in different 32-row blocks takes
 //     (suffix of j's block) (blocks between) (prefix of i's block), so no exponential grows
 //     and none is taken of a difference of large sums; inside a block G_i - G_j is a
 //     difference of sums over at most 32 rows. Gates below -110 count as -110, whose
 //     exponential is 0 in fp32 like that of anything below.
 //
-// Roles (15 warps), which meet through mbarriers only:
+// Roles (16 warps), which meet through mbarriers only:
 //   warps 0-3   scores: P = Q K^T out of TMEM, times the decays, rounded to bf16 into TMEM, where
-//               P V takes its left operand (row i is TMEM lane i; a warp is a 32-row block)
-//   warps 4-7   state: lane i holds row i of S, 64 columns in registers; adds a chunk's three
+//               P V takes its left operand (row i is TMEM lane i; a warp is a 32-row block); then
+//               the chunk before's output, o = P V + e^G (Q S), out of TMEM to global memory
+//   warps 4-7   state: lane i holds row i of S, 64 columns in registers; adds a chunk's
 //               partial products and writes S as bf16 to shared memory for the next Q S
-//   warps 8-11  values: the three terms of the decayed V to shared memory; the chunk's output
-//               o = P V + e^G (Q S) out of TMEM to global memory
+//   warps 8-11  values: the three terms of the decayed V to shared memory, 64 rows at a time, so
+//               that one half is written while the other is multiplied
 //   warp 12     loader: q, k, v by TMA, two stages. It clears the rows of k and v behind a
 //               sequence's end (they are another's), so that nothing of them enters a product
-//   warp 13     issues every tcgen05.mma
-//   warp 14     gates: block-wise prefix and suffix sums, a chunk ahead
-// TMEM: P 128 columns, bf16 P 64, P V 64, Q S 64, three state terms 192: all 512. Shared memory:
+//   warp 13     issues the state's products, warp 14 the scores', Q S and P V
+//   warp 15     gates: block-wise prefix and suffix sums, a chunk ahead
+// The loops over pieces of a tile are mostly not unrolled: every role runs its code once per
+// chunk, all at the same time, and the kernel is bound by instruction fetch where their sum
+// outgrows the cache (132 KB of code ran a chunk in 7.2 us, the same loops rolled up, 77 KB, in
+// 3.3 us).
+// TMEM: P 128 columns, bf16 P 64, P V 64, Q S 2 x 64, the state's terms 2 x 64: all 512. Shared memory:
 // 2 x 80 KiB of stages, 48 KiB of decayed V, 16 KiB of bf16 state.
 // Every wait is bounded; on expiry the CTA records KDA_ERR_TIMEOUT, drains its copies and
 // products, frees TMEM and exits.
@@ -53,8 +57,8 @@ using namespace sm100;
 
 constexpr int kC = 128;                 // tokens per chunk
 constexpr int kNV = 64;                 // value columns per CTA
-constexpr int kThreads = 15 * 32;
-constexpr int kLoadWarp = 12, kMmaWarp = 13;   // the last warp is the gates'
+constexpr int kThreads = 16 * 32;
+constexpr int kLoadWarp = 12, kStateMma = 13, kOutMma = 14;   // the last warp is the gates'
 
 constexpr uint32_t kPanel = 16384;      // 128 rows x 128 bytes, 128-byte swizzle
 constexpr uint32_t ST_Q = 0, ST_K = 2 * kPanel, ST_V = 4 * kPanel, kStage = 5 * kPanel;
@@ -63,12 +67,13 @@ constexpr uint32_t OFF_SB = OFF_VH + 3 * kPanel;    // bf16 state
 constexpr uint32_t OFF_GATE = OFF_SB + kPanel;      // per stage: loc[128], suf[128], tot[4]
 constexpr uint32_t kGateBytes = (2 * kC + 4) * 4;
 constexpr uint32_t OFF_BAR = OFF_GATE + 2 * kGateBytes;
-constexpr uint32_t OFF_MISC = OFF_BAR + 18 * 8;     // TMEM address, abort flag
+constexpr uint32_t kHalf = 3 * kPanel / 2;           // 64 rows of the three terms
+constexpr uint32_t OFF_MISC = OFF_BAR + 24 * 8;     // TMEM address, abort flag
 constexpr uint32_t kSmem = OFF_MISC + 16;
 static_assert(kSmem <= 232448, "shared memory");
 static_assert(OFF_BAR % 8 == 0 && OFF_GATE % 16 == 0 && kGateBytes % 16 == 0, "alignment");
 
-constexpr uint32_t TM_P = 0, TM_PB = 128, TM_O1 = 192, TM_O2 = 256, TM_KV = 320;
+constexpr uint32_t TM_P = 0, TM_PB = 128, TM_O1 = 192, TM_O2 = 256 /* two */, TM_KV = 384;
 constexpr int kTmemCols = 512;
 
 struct ChunkArgs {
@@ -88,6 +93,19 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 __device__ __forceinline__ float lo_bf(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_bf(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+// 2^x, at most 2 units in the last place off.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// One box into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -109,25 +127,29 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     const int nchunks = (int)((sl.end - sl.begin + kC - 1) / kC);
     const int j0 = tile * kNV;
 
-    // barriers: each role's waits on one count the chunks (two of a kind: one per stage)
-    uint32_t nb = sb + OFF_BAR;
-    const uint32_t b_full = nb, b_empty = nb + 16, b_gfull = nb + 32, b_gempty = nb + 48,
-                   b_p = nb + 64, b_pb = nb + 72, b_vh = nb + 80, b_kv = nb + 88,
-                   b_kvfree = nb + 96, b_s = nb + 104, b_sfree = nb + 112, b_o = nb + 120,
-                   b_ofree = nb + 128, b_tail = nb + 136;
+    // barriers: each counts the chunks (pairs: one per stage; b_vh: one per half of the rows)
+    const uint32_t nb = sb + OFF_BAR;
+    const uint32_t b_full = nb, b_qkfree = nb + 16, b_vfree = nb + 32, b_gfull = nb + 48,
+                   b_gfree = nb + 64, b_vh = nb + 80, b_vh0free = nb + 96, b_kv = nb + 104,
+                   b_kvfree = nb + 112, b_p = nb + 120, b_pb = nb + 128, b_s = nb + 136,
+                   b_sfree = nb + 144, b_o = nb + 152, b_ofree = nb + 160, b_tail = nb + 168,
+                   b_vfull = nb + 176;
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(sm + OFF_MISC);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 1);
+            mbar_init(b_full + 8 * i, 1);                 // q, k
+            mbar_init(b_vfull + 8 * i, 1);
+            mbar_init(b_qkfree + 8 * i, kOut ? 2 : 1);    // both issuing warps have read
+            mbar_init(b_vfree + 8 * i, 1);
             mbar_init(b_gfull + 8 * i, 1);
-            mbar_init(b_gempty + 8 * i, kOut ? 12 : 8);   // one per reading warp
+            mbar_init(b_gfree + 8 * i, kOut ? 12 : 8);    // one per reading warp
+            mbar_init(b_vh + 8 * i, 128);
         }
-        mbar_init(b_p, 1);
-        mbar_init(b_pb, 128);
-        mbar_init(b_vh, 128);
+        mbar_init(b_vh0free, 1);
         mbar_init(b_kv, 1);
         mbar_init(b_kvfree, 128);
+        mbar_init(b_p, 1);
+        mbar_init(b_pb, 128);
         mbar_init(b_s, 128);
         mbar_init(b_sfree, 1);
         mbar_init(b_o, 1);
@@ -151,7 +173,13 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
 
     // every lane waits; a warp goes on together or not at all
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait(bar, parity & 1u, args.budget);
+        bool ok = mbar_try_wait(bar, parity & 1u);
+        if (!ok) {
+            const long long t0 = clock64();
+#pragma unroll 1
+            do ok = mbar_try_wait_sleep(bar, parity & 1u);
+            while (!ok && clock64() - t0 <= args.budget);
+        }
         if (__all_sync(0xffffffffu, ok)) return true;
         if (lane == 0) set_device_error(p.err, DEV_TIMEOUT);
         return false;
@@ -163,58 +191,129 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
 
     if (warp < 4) {
         // ============================================================ scores
-        if (kOut) {
-            for (int c = 0; c < nchunks; ++c) {
-                if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
-                const float* gt = gates(c);
-                const float loc = gt[row];
-                float f[4];   // what the suffix of block b lacks to reach this row
-                f[3] = 1.f;
-                const float pre = expf(loc);
+        // o = P V + e^G (Q S) of chunk c: this thread's row, 32 columns at a time. Four lanes
+        // exchange their rows' 16-byte pieces, so that a store covers 64 bytes of each of 8 rows
+        // instead of 16 bytes of each of 32.
+        auto store = [&](int c, float er) {
+            const int valid = rows_of(c), r0 = 32 * warp + (lane & ~3);
+            const bool b0 = lane & 1, b1 = lane & 2;
+            __nv_bfloat16* to =
+                static_cast<__nv_bfloat16*>(p.o) +
+                ((sl.begin + (long long)c * kC + r0) * p.H + h) * (long long)p.dv + j0 +
+                8 * (lane & 3);
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t u[4][4];
+                {
+                    float x[32], y[32];
+                    tmem_ld32(tbase + lq + TM_O1 + 32 * hf, x);
+                    tmem_ld32(tbase + lq + TM_O2 + 64 * (c & 1) + 32 * hf, y);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int b = 0; b < 3; ++b) {
-                    float between = 0.f;
-#pragma unroll
-                    for (int m = 1; m < 3; ++m)
-                        if (m > b && m < warp) between += gt[2 * kC + m];
-                    f[b] = pre * expf(between);
+                    for (int i = 0; i < 16; ++i)
+                        u[i / 4][i % 4] = pack2(fmaf(er, y[2 * i], x[2 * i]),
+                                                fmaf(er, y[2 * i + 1], x[2 * i + 1]));
                 }
-                if (!wait(b_p, c)) break;
-                // the bf16 scores are free once the previous chunk's P V is done
-                if (c > 0 && !wait(b_o, c - 1)) break;
-                tc_fence_after();
+                if (hf == 1) {
+                    tc_fence_before();
+                    mbar_arrive(b_ofree);
+                }
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t pk[16];
-                    if (b > warp) {
+                for (int w = 0; w < 4; ++w) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
-                    } else {
-                        float x[32];
-                        tmem_ld32(tbase + lq + TM_P + 32 * b, x);
-                        tmem_ld_wait();
-                        const float* at = gt + 32 * b + (b < warp ? kC : 0);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 y = *reinterpret_cast<const float4*>(at + i);
-                            const float z[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x[i + e] = b < warp ? x[i + e] * (f[b] * z[e])
-                                           : i + e <= lane ? x[i + e] * __expf(loc - z[e])
-                                                           : 0.f;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = pack2(x[2 * i], x[2 * i + 1]);
+                    for (int m = 0; m < 4; m += 2) {
+                        const uint32_t got =
+                            __shfl_xor_sync(0xffffffffu, b0 ? u[m][w] : u[m + 1][w], 1);
+                        if (b0) u[m][w] = got;
+                        else u[m + 1][w] = got;
                     }
-                    tmem_st16u(tbase + lq + TM_PB + 16 * b, pk);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t got =
+                            __shfl_xor_sync(0xffffffffu, b1 ? u[m][w] : u[m + 2][w], 2);
+                        if (b1) u[m][w] = got;
+                        else u[m + 2][w] = got;
+                    }
+                }
+                if (j0 + 32 * hf + 8 * (lane & 3) < p.dv) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)   // row r0 + m
+                        if (r0 + m < valid)
+                            *reinterpret_cast<uint4*>(to + (long long)m * p.H * p.dv + 32 * hf) =
+                                make_uint4(u[m][0], u[m][1], u[m][2], u[m][3]);
+                }
+            }
+        };
+        // chunk c's scores, then, while chunk c + 1's are multiplied, chunk c - 1's output
+        const uint32_t pb = tbase + lq + TM_PB;
+        float er_last = 0.f;
+#pragma unroll 1
+        for (int c = 0; kOut && nchunks > 0 && c <= nchunks; ++c) {
+            float er = 0.f;
+            if (c < nchunks) {
+                if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
+                if (!wait(b_p, c)) break;
+            }
+            // P V of the chunk before is done: its bf16 scores' columns are free and its output
+            // is there
+            if (c > 0 && !wait(b_o, c - 1)) break;
+            tc_fence_after();
+            if (c < nchunks) {
+                const float* gt = gates(c);
+                const float loc = gt[row], pre = ex2(loc);
+                // the blocks before this row's: what the suffix of block b lacks to reach the row
+                float between = 1.f;
+#pragma unroll 1
+                for (int b = warp - 1; b >= 0; --b) {
+                    float x[32];
+                    tmem_ld32(tbase + lq + TM_P + 32 * b, x);
+                    const float f = pre * between;
+                    between *= ex2(gt[2 * kC + b]);
+                    const float* at = gt + kC + 32 * b;
+                    uint32_t pk[16];
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(at + i);
+                        pk[i / 2] = pack2(x[i] * (f * y.x), x[i + 1] * (f * y.y));
+                        pk[i / 2 + 1] = pack2(x[i + 2] * (f * y.z), x[i + 3] * (f * y.w));
+                    }
+                    tmem_st16u(pb + 16 * b, pk);
+                }
+                er = pre * between;
+                {   // the row's own block
+                    float x[32];
+                    tmem_ld32(tbase + lq + TM_P + 32 * warp, x);
+                    const float* at = gt + 32 * warp;
+                    uint32_t pk[16];
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(at + i);
+                        const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[i + e] = i + e <= lane ? x[i + e] * ex2(loc - z[e]) : 0.f;
+                        pk[i / 2] = pack2(x[i], x[i + 1]);
+                        pk[i / 2 + 1] = pack2(x[i + 2], x[i + 3]);
+                    }
+                    tmem_st16u(pb + 16 * warp, pk);
+                }
+                if (c == 0) {   // the blocks behind stay zero: no later chunk writes them
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) pk[i] = 0u;
+#pragma unroll 1
+                    for (int b = warp + 1; b < 4; ++b) tmem_st16u(pb + 16 * b, pk);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(b_pb);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_gempty + 8 * (c & 1));
+                if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
             }
+            if (c > 0) store(c - 1, er_last);
+            er_last = er;
         }
     } else if (warp < 8) {
         // ============================================================ state
@@ -249,26 +348,21 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
             const float4 tot = *reinterpret_cast<const float4*>(gates(c) + 2 * kC);
             const float sum = (tot.x + tot.y) + (tot.z + tot.w);
-            const float e = expf(sum);
+            const float e = exp2f(sum);
             decay += sum;
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_gempty + 8 * (c & 1));
+            if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
             if (!wait(b_kv, c)) break;
             tc_fence_after();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[32], y[32];
-                // the smallest terms first
-                tmem_ld32(tbase + lq + TM_KV + 128 + 32 * half, x);
-                tmem_ld32(tbase + lq + TM_KV + 64 + 32 * half, y);
+            for (int q = 0; q < 4; ++q) {
+                float x[16], y[16];
+                tmem_ld16(tbase + lq + TM_KV + 16 * q, x);
+                tmem_ld16(tbase + lq + TM_KV + 64 + 16 * q, y);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] += y[i];
-                tmem_ld32(tbase + lq + TM_KV + 32 * half, y);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    S[32 * half + i] = fmaf(e, S[32 * half + i], x[i] + y[i]);
+                for (int i = 0; i < 16; ++i)
+                    S[16 * q + i] = fmaf(e, S[16 * q + i], x[i] + y[i]);
             }
             tc_fence_before();
             mbar_arrive(b_kvfree);
@@ -286,106 +380,106 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                     *reinterpret_cast<float4*>(out + at + i) =
                         make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
         }
-        if (!kOut && tile == 0 && row == 0) p.seg_decay[(size_t)g * p.H + h] = expf(decay);
+        if (!kOut && tile == 0 && row == 0) p.seg_decay[(size_t)g * p.H + h] = exp2f(decay);
     } else if (warp < 12) {
-        // ============================================================ values and outputs
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o);
-        auto store = [&](int c, float er) -> bool {
-            if (!wait(b_o, c)) return false;
-            tc_fence_after();
-            const bool mine = row < rows_of(c);
-            __nv_bfloat16* to =
-                o + ((sl.begin + (long long)c * kC + row) * p.H + h) * (long long)p.dv + j0;
-            uint32_t pk[32];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[32], y[32];
-                tmem_ld32(tbase + lq + TM_O1 + 32 * half, x);
-                tmem_ld32(tbase + lq + TM_O2 + 32 * half, y);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    pk[16 * half + i] = pack2(fmaf(er, y[2 * i], x[2 * i]),
-                                              fmaf(er, y[2 * i + 1], x[2 * i + 1]));
-            }
-            tc_fence_before();
-            mbar_arrive(b_ofree);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (mine && j0 + 8 * i < p.dv)
-                    *reinterpret_cast<uint4*>(to + 8 * i) =
-                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-            return true;
-        };
-        float er_last = 0.f;
-        bool ok = true;
+        // ============================================================ values
+        const int vr = tid & 63, vcol = 4 * (tid >> 6 & 1);   // value row (mod 64), first 16 bytes
+#pragma unroll 1
         for (int c = 0; c < nchunks; ++c) {
-            ok = wait(b_gfull + 8 * (c & 1), c >> 1) && wait(b_full + 8 * (c & 1), c >> 1);
-            if (!ok) break;
+            if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
             const float* gt = gates(c);
-            const int block = row >> 5;
-            float before = 0.f, behind = 0.f;
+            float ek[2];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float t = gt[2 * kC + m];
-                if (m < block) before += t;
-                if (m > block) behind += t;
+            for (int hf = 0; hf < 2; ++hf) {   // rows vr, 64 + vr
+                float behind = 0.f;
+#pragma unroll
+                for (int m = 1; m < 4; ++m)
+                    if (m > 2 * hf + (vr >> 5)) behind += gt[2 * kC + m];
+                ek[hf] = ex2(behind) * gt[kC + 64 * hf + vr];
             }
-            const float er = expf(before) * expf(gt[row]);
-            const float ek = expf(behind) * gt[kC + row];
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_gempty + 8 * (c & 1));
-            // the decayed V is free once the previous chunk's product is done
-            ok = c == 0 || wait(b_kv, c - 1);
-            if (!ok) break;
-            const uint8_t* v = sm + (c & 1) * kStage + ST_V + row * 128;
-            uint8_t* vh = sm + OFF_VH + row * 128;
+            if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
+            if (!wait(b_vfull + 8 * (c & 1), c >> 1)) break;
+            const uint8_t* v = sm + (c & 1) * kStage + ST_V + vr * 128;
+            uint8_t* vh = sm + OFF_VH + vr * 128;
+            bool ok = true;
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                // a half is free once the previous chunk's product with it is done
+                ok = c == 0 || wait(hf ? b_kv : b_vh0free, c - 1);
+                if (!ok) break;
+                const float f = hf ? ek[1] : ek[0];
+#pragma unroll 2
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t ch = (uint32_t)((vcol + i) ^ (vr & 7)) << 4;
+                    const uint4 u = *reinterpret_cast<const uint4*>(v + hf * (kPanel / 2) + ch);
+                    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t t[3][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t ch = (uint32_t)(i ^ (row & 7)) << 4;
-                const uint4 u = *reinterpret_cast<const uint4*>(v + ch);
-                const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-                uint32_t t[3][4];
+                    for (int e = 0; e < 4; ++e) {
+                        float a = f * lo_bf(in[e]), b = f * hi_bf(in[e]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float a = ek * lo_bf(in[e]), b = ek * hi_bf(in[e]);
-#pragma unroll
-                    for (int m = 0; m < 3; ++m) {
-                        t[m][e] = pack2(a, b);
-                        a -= lo_bf(t[m][e]);
-                        b -= hi_bf(t[m][e]);
+                        for (int m = 0; m < 3; ++m) {
+                            t[m][e] = pack2(a, b);
+                            a -= lo_bf(t[m][e]);
+                            b -= hi_bf(t[m][e]);
+                        }
                     }
-                }
 #pragma unroll
-                for (int m = 0; m < 3; ++m)
-                    *reinterpret_cast<uint4*>(vh + m * kPanel + ch) =
-                        make_uint4(t[m][0], t[m][1], t[m][2], t[m][3]);
+                    for (int m = 0; m < 3; ++m)
+                        *reinterpret_cast<uint4*>(vh + hf * kHalf + m * (kPanel / 2) + ch) =
+                            make_uint4(t[m][0], t[m][1], t[m][2], t[m][3]);
+                }
+                fence_proxy_async();
+                mbar_arrive(b_vh + 8 * hf);
             }
-            fence_proxy_async();
-            mbar_arrive(b_vh);
-            if (kOut && c > 0 && !(ok = store(c - 1, er_last))) break;
-            er_last = er;
+            if (!ok) break;
         }
-        if (kOut && ok && nchunks > 0) store(nchunks - 1, er_last);
     } else if (warp == kLoadWarp) {
         // ============================================================ loader
-        const uint32_t bytes = (kOut ? 5u : 3u) * kPanel;
-        for (int c = 0; c < nchunks; ++c) {
+        // Loads of a chunk follow its stage's release, a chunk before their use; its tiles are
+        // fetched into L2 two chunks before that, so that they then take an L2 hit's time.
+        const uint32_t qk_bytes = (kOut ? 4u : 2u) * kPanel;
+        auto ahead = [&](int c) {
+            if (c >= nchunks || lane != 0) return;
+            const int t = (int)(sl.begin + (long long)c * kC);
+            tma_prefetch_3d(&maps.k, 0, hk, t);
+            tma_prefetch_3d(&maps.k, 64, hk, t);
+            if (kOut) {
+                tma_prefetch_3d(&maps.q, 0, hk, t);
+                tma_prefetch_3d(&maps.q, 64, hk, t);
+            }
+            tma_prefetch_3d(&maps.v, j0, h, t);
+        };
+#pragma unroll 1
+        for (int c = -2; c < nchunks; ++c) {
             const int s = c & 1;
+            ahead(c + 4);
+            if (c < 0) continue;
             if (args.debug_stall && !wait(b_tail, 0)) break;
-            if (c >= 2 && !wait(b_empty + 8 * s, (c >> 1) - 1)) break;
+            if (c >= 2 && !wait(b_qkfree + 8 * s, (c >> 1) - 1)) break;
             const int valid = rows_of(c);
-            const uint32_t st = sb + s * kStage, bar = valid < kC ? b_tail : b_full + 8 * s;
+            const int t = (int)(sl.begin + (long long)c * kC);
+            const uint32_t st = sb + s * kStage;
+            const uint32_t qk_bar = valid < kC ? b_tail : b_full + 8 * s;
             if (lane == 0) {
-                const int t = (int)(sl.begin + (long long)c * kC);
-                mbar_arrive_expect_tx(bar, bytes);
-                tma_load_3d(st + ST_K, &maps.k, bar, 0, hk, t);
-                tma_load_3d(st + ST_K + kPanel, &maps.k, bar, 64, hk, t);
-                tma_load_3d(st + ST_V, &maps.v, bar, j0, h, t);
+                mbar_arrive_expect_tx(qk_bar, qk_bytes + (valid < kC ? kPanel : 0u));
+                tma_load_3d(st + ST_K, &maps.k, qk_bar, 0, hk, t);
+                tma_load_3d(st + ST_K + kPanel, &maps.k, qk_bar, 64, hk, t);
                 if (kOut) {
-                    tma_load_3d(st + ST_Q, &maps.q, bar, 0, hk, t);
-                    tma_load_3d(st + ST_Q + kPanel, &maps.q, bar, 64, hk, t);
+                    tma_load_3d(st + ST_Q, &maps.q, qk_bar, 0, hk, t);
+                    tma_load_3d(st + ST_Q + kPanel, &maps.q, qk_bar, 64, hk, t);
                 }
+            }
+            __syncwarp();
+            if (c >= 2 && !wait(b_vfree + 8 * s, (c >> 1) - 1)) {
+                // the tail's v never comes: nothing waits for b_tail's phase then
+                break;
+            }
+            if (lane == 0) {
+                const uint32_t bar = valid < kC ? b_tail : b_vfull + 8 * s;
+                if (valid == kC) mbar_arrive_expect_tx(bar, kPanel);
+                tma_load_3d(st + ST_V, &maps.v, bar, j0, h, t);
             }
             __syncwarp();
             if (valid < kC) {   // a sequence's last chunk
@@ -398,76 +492,108 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                             make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_full + 8 * s);
+                if (lane == 0) {
+                    mbar_arrive(b_full + 8 * s);
+                    mbar_arrive(b_vfull + 8 * s);
+                }
             }
         }
         // copies in flight land before the shared memory goes away (bounded; a completed phase
         // returns at once)
-        for (int c = max(0, nchunks - 2); c < nchunks; ++c)
-            mbar_wait(rows_of(c) < kC ? b_tail : b_full + 8 * (c & 1),
-                      rows_of(c) < kC ? 0u : (uint32_t)((c >> 1) & 1), args.budget);
-    } else if (warp == kMmaWarp) {
-        // ============================================================ products
-        const uint64_t dK = sw128_desc(0, 16, 1024);          // K-major
-        const uint64_t dM = sw128_desc(0, kPanel, 1024);      // MN-major, 128-row panels
-        const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, kNV, 0, 1),
-                       id_kv = idesc_bf16(128, 3 * kNV, 1, 1);
-        auto scores = [&](int c) -> bool {
-            if (!wait(b_full + 8 * (c & 1), c >> 1)) return false;
-            tc_fence_after();
-            const uint32_t st = sb + (c & 1) * kStage;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                umma_f16_warp(tbase + TM_P,
-                              desc_at(dK, st + ST_Q + (s >> 2) * kPanel + (s & 3) * 32),
-                              desc_at(dK, st + ST_K + (s >> 2) * kPanel + (s & 3) * 32), id_qk,
-                              s > 0);
-            umma_commit_warp(b_p);
-            return true;
-        };
-        int done = 0;   // chunks whose products were all issued
-        if (!kOut || nchunks == 0 || scores(0)) {
-            for (int c = 0; c < nchunks; ++c) {
-                const uint32_t st = sb + (c & 1) * kStage;
-                if (!wait(b_vh, c)) break;
-                if (c > 0 && !wait(b_kvfree, c - 1)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    umma_f16_warp(tbase + TM_KV, desc_at(dM, st + ST_K + 2048 * s),
-                                  desc_at(dM, sb + OFF_VH + 2048 * s), id_kv, s > 0);
-                umma_commit_warp(b_kv);
-                if (kOut) {
-                    if (!wait(b_s, c)) break;
-                    if (c > 0 && !wait(b_ofree, c - 1)) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        umma_f16_warp(tbase + TM_O2,
-                                      desc_at(dK, st + ST_Q + (s >> 2) * kPanel + (s & 3) * 32),
-                                      desc_at(dM, sb + OFF_SB + 2048 * s), id_o, s > 0);
-                    umma_commit_warp(b_sfree);
-                    if (!wait(b_pb, c)) break;
-                    tc_fence_after();
-                    if (c + 1 < nchunks && !scores(c + 1)) break;
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        umma_f16_ts_warp(tbase + TM_O1, tbase + TM_PB + 8 * s,
-                                         desc_at(dM, st + ST_V + 2048 * s), id_o, s > 0);
-                    umma_commit_warp(b_o);
-                }
-                umma_commit_warp(b_empty + 8 * (c & 1));
-                done = c + 1;
+        for (int c = max(0, nchunks - 2); c < nchunks; ++c) {
+            const uint32_t par = (uint32_t)((c >> 1) & 1);
+            if (rows_of(c) < kC) {
+                mbar_wait(b_tail, 0u, args.budget);
+            } else {
+                mbar_wait(b_full + 8 * (c & 1), par, args.budget);
+                mbar_wait(b_vfull + 8 * (c & 1), par, args.budget);
             }
         }
+    } else if (warp == kStateMma) {
+        // ============================================================ the state's products
+        const uint64_t dM = sw128_desc(0, kPanel, 1024);         // MN-major, 128-row panels
+        const uint64_t dV = sw128_desc(0, kPanel / 2, 1024);     // MN-major, 64-row panels
+        const uint32_t id2 = idesc_bf16(128, 2 * kNV, 1, 1), id1 = idesc_bf16(128, kNV, 1, 1);
+        // 64 rows: the first two terms side by side, then the third onto the second's sum
+        auto half = [&](uint32_t k, uint32_t v, bool add) {
+#pragma unroll 2
+            for (int s = 0; s < 4; ++s) {
+                umma_f16_warp(tbase + TM_KV, desc_at(dM, k + 2048 * s), desc_at(dV, v + 2048 * s),
+                              id2, add || s > 0);
+                umma_f16_warp(tbase + TM_KV + kNV, desc_at(dM, k + 2048 * s),
+                              desc_at(dV, v + kPanel + 2048 * s), id1, 1);
+            }
+        };
+        int c = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (; c < nchunks; ++c) {
+            const uint32_t k = sb + (c & 1) * kStage + ST_K;
+            ok = wait(b_full + 8 * (c & 1), c >> 1) && (c == 0 || wait(b_kvfree, c - 1));
+#pragma unroll 1
+            for (int hf = 0; ok && hf < 2; ++hf) {
+                ok = wait(b_vh + 8 * hf, c);
+                if (!ok) break;
+                tc_fence_after();
+                half(k + hf * (kPanel / 2), sb + OFF_VH + hf * kHalf, hf);
+                umma_commit_warp(hf ? b_kv : b_vh0free);
+            }
+            if (!ok) break;
+            umma_commit_warp(b_qkfree + 8 * (c & 1));
+            if (!kOut) umma_commit_warp(b_vfree + 8 * (c & 1));
+        }
         // every product issued is finished before TMEM and the shared memory go away: the last
-        // commit, and on the way out after an expired wait one more for what was issued since
-        if (done == nchunks) {
-            if (nchunks > 0) mbar_wait(b_empty + 8 * ((nchunks - 1) & 1),
-                                       (uint32_t)(((nchunks - 1) >> 1) & 1), args.budget);
-        } else {
-            umma_commit_warp(b_empty + 8 * (done & 1));
-            mbar_wait(b_empty + 8 * (done & 1), (uint32_t)((done >> 1) & 1), args.budget);
+        // chunk's, or, on the way out after an expired wait, what this last commit covers
+        if (c < nchunks) umma_commit_warp(b_kv);
+        if (nchunks > 0) mbar_wait(b_kv, (uint32_t)(min(c, nchunks - 1) & 1), args.budget);
+    } else if (warp == kOutMma) {
+        // ============================================================ scores, Q S and P V
+        const uint64_t dK = sw128_desc(0, 16, 1024);          // K-major
+        const uint64_t dM = sw128_desc(0, kPanel, 1024);      // MN-major, 128-row panels
+        const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, kNV, 0, 1);
+        // iteration c issues chunk c's Q S, which frees its q and k; then, as soon as the score
+        // warps have read chunk c's scores, chunk c + 1's; then chunk c's P V
+        int c = kOut && nchunks > 0 ? -1 : nchunks;
+#pragma unroll 1
+        for (; c < nchunks; ++c) {
+            const uint32_t st = sb + (c & 1) * kStage, sn = sb + ((c + 1) & 1) * kStage;
+            if (c >= 0) {
+                if (!wait(b_s, c)) break;
+                tc_fence_after();   // (its columns of O2 are free: P V of c - 1 went after their reader)
+#pragma unroll 4
+                for (int s = 0; s < 8; ++s)
+                    umma_f16_warp(tbase + TM_O2 + 64 * (c & 1),
+                                  desc_at(dK, st + ST_Q + (s >> 2) * kPanel + (s & 3) * 32),
+                                  desc_at(dM, sb + OFF_SB + 2048 * s), id_o, s > 0);
+                umma_commit_warp(b_sfree);
+                umma_commit_warp(b_qkfree + 8 * (c & 1));
+                if (!wait(b_pb, c)) break;
+            }
+            if (c + 1 < nchunks) {
+                if (!wait(b_full + 8 * ((c + 1) & 1), (c + 1) >> 1)) break;
+                tc_fence_after();
+#pragma unroll 4
+                for (int s = 0; s < 8; ++s)
+                    umma_f16_warp(tbase + TM_P,
+                                  desc_at(dK, sn + ST_Q + (s >> 2) * kPanel + (s & 3) * 32),
+                                  desc_at(dK, sn + ST_K + (s >> 2) * kPanel + (s & 3) * 32), id_qk,
+                                  s > 0);
+                umma_commit_warp(b_p);
+            }
+            if (c < 0) continue;
+            if (c > 0 && !wait(b_ofree, c - 1)) break;
+            if (!wait(b_vfull + 8 * (c & 1), c >> 1)) break;
+            tc_fence_after();
+#pragma unroll 4
+            for (int s = 0; s < 8; ++s)
+                umma_f16_ts_warp(tbase + TM_O1, tbase + TM_PB + 8 * s,
+                                 desc_at(dM, st + ST_V + 2048 * s), id_o, s > 0);
+            umma_commit_warp(b_vfree + 8 * (c & 1));
+            umma_commit_warp(b_o);
+        }
+        if (kOut && nchunks > 0) {
+            if (c < nchunks) umma_commit_warp(b_o);
+            mbar_wait(b_o, (uint32_t)(max(0, min(c, nchunks - 1)) & 1), args.budget);
         }
     } else {
         // ============================================================ gates
@@ -479,13 +605,13 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             for (int e = 0; e < 4; ++e) {
                 float y = 0.f;
                 if (4 * lane + e < valid) y = p.log_g[p.gate_head ? h : (t + e) * p.H + h];
-                to[e] = y < -110.f ? -110.f : y;
+                to[e] = 1.4426950408889634f * (y < -110.f ? -110.f : y);   // in powers of two
             }
         };
         fetch(0, x);
         for (int c = 0; c < nchunks; ++c) {
             fetch(c + 1, nx);
-            if (c >= 2 && !wait(b_gempty + 8 * (c & 1), (c >> 1) - 1)) break;
+            if (c >= 2 && !wait(b_gfree + 8 * (c & 1), (c >> 1) - 1)) break;
             float* gt = gates(c);
             // inclusive prefix and exclusive suffix sums in the lane's 32-row block (8 lanes)
             const float a1 = x[0] + x[1], a2 = a1 + x[2], all = a2 + x[3];
@@ -505,7 +631,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 make_float4(pre + x[0], pre + a1, pre + a2, pre + all);
             const float s2 = suf + x[3], s1 = s2 + x[2], s0 = s1 + x[1];
             *reinterpret_cast<float4*>(gt + kC + 4 * lane) =
-                make_float4(expf(s0), expf(s1), expf(s2), expf(suf));
+                make_float4(ex2(s0), ex2(s1), ex2(s2), ex2(suf));
             if ((lane & 7) == 0) gt[2 * kC + (lane >> 3)] = down;
             __syncwarp();
             if (lane == 0) mbar_arrive(b_gfull + 8 * (c & 1));
