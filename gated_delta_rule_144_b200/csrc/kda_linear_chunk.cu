@@ -24,11 +24,12 @@
 // Roles (16 warps), which meet through mbarriers only:
 //   warps 0-3   scores: P = Q K^T out of TMEM, times the decays, rounded to bf16 into TMEM, where
 //               P V takes its left operand (row i is TMEM lane i; a warp is a 32-row block); then
-//               the chunk before's output, o = P V + e^G (Q S), out of TMEM to global memory
+//               the chunk before's output, o = P V + e^G (Q S), out of TMEM, staged in shared
+//               memory and stored by TMA (a sequence's last, partial chunk row by row)
 //   warps 4-7   state: lane i holds row i of S, 64 columns in registers; adds a chunk's
 //               partial products and writes S as bf16 to shared memory for the next Q S
-//   warps 8-11  values: the three terms of the decayed V to shared memory, 64 rows at a time, so
-//               that one half is written while the other is multiplied
+//   warps 8-11  values: the three terms of the decayed V to shared memory, 32 rows at a time in
+//               two buffers, so that one is written while the other is multiplied
 //   warp 12     loader: q, k, v by TMA, two stages. It clears the rows of k and v behind a
 //               sequence's end (they are another's), so that nothing of them enters a product
 //   warp 13     issues the state's products, warp 14 the scores', Q S and P V
@@ -38,7 +39,7 @@
 // outgrows the cache (132 KB of code ran a chunk in 7.2 us, the same loops rolled up, 77 KB, in
 // 3.3 us).
 // TMEM: P 128 columns, bf16 P 64, P V 64, Q S 2 x 64, the state's terms 2 x 64: all 512. Shared memory:
-// 2 x 80 KiB of stages, 48 KiB of decayed V, 16 KiB of bf16 state.
+// 2 x 80 KiB of stages, 24 KiB of decayed V, 16 KiB of bf16 state, 16 KiB of output.
 // Every wait is bounded; on expiry the CTA records KDA_ERR_TIMEOUT, drains its copies and
 // products, frees TMEM and exits.
 
@@ -62,13 +63,15 @@ constexpr int kLoadWarp = 12, kStateMma = 13, kOutMma = 14;   // the last warp i
 
 constexpr uint32_t kPanel = 16384;      // 128 rows x 128 bytes, 128-byte swizzle
 constexpr uint32_t ST_Q = 0, ST_K = 2 * kPanel, ST_V = 4 * kPanel, kStage = 5 * kPanel;
-constexpr uint32_t OFF_VH = 2 * kStage;             // three terms of the decayed V
-constexpr uint32_t OFF_SB = OFF_VH + 3 * kPanel;    // bf16 state
-constexpr uint32_t OFF_GATE = OFF_SB + kPanel;      // per stage: loc[128], suf[128], tot[4]
+constexpr uint32_t kQuarter = kPanel / 4;           // 32 rows of one term of the decayed V
+constexpr uint32_t kVH = 3 * kQuarter;
+constexpr uint32_t OFF_VH = 2 * kStage;             // two buffers of 32 rows of the three terms
+constexpr uint32_t OFF_SB = OFF_VH + 2 * kVH;       // bf16 state
+constexpr uint32_t OFF_OUT = OFF_SB + kPanel;       // output on its way to global memory
+constexpr uint32_t OFF_GATE = OFF_OUT + kPanel;      // per stage: loc[128], suf[128], tot[4]
 constexpr uint32_t kGateBytes = (2 * kC + 4) * 4;
 constexpr uint32_t OFF_BAR = OFF_GATE + 2 * kGateBytes;
-constexpr uint32_t kHalf = 3 * kPanel / 2;           // 64 rows of the three terms
-constexpr uint32_t OFF_MISC = OFF_BAR + 24 * 8;     // TMEM address, abort flag
+constexpr uint32_t OFF_MISC = OFF_BAR + 26 * 8;     // TMEM address, abort flag
 constexpr uint32_t kSmem = OFF_MISC + 16;
 static_assert(kSmem <= 232448, "shared memory");
 static_assert(OFF_BAR % 8 == 0 && OFF_GATE % 16 == 0 && kGateBytes % 16 == 0, "alignment");
@@ -79,12 +82,12 @@ constexpr int kTmemCols = 512;
 struct ChunkArgs {
     LinearParams p;
     int tiles;              // 64-column tiles of dv
-    long long budget;       // cycles a wait may take
+    uint32_t budget;        // cycles a wait may take
     int debug_stall;
 };
 
 struct ChunkMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -99,12 +102,47 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// mbar_wait in few instructions: a first test, then suspending ones until `budget` cycles passed.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32_t budget) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t1;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u32 t0, %%clock;\n\t"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u32 t1, %%clock;\n\t"
+        "sub.u32 t1, t1, t0;\n\t"
+        "setp.le.u32 q, t1, %3;\n\t"
+        "@q bra AGAIN;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(budget), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void mul2(float& a, float& b, float f) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(a), "+f"(b) : "f"(f));
+}
+__device__ __forceinline__ void sub2(float& a, float& b, float c, float d) {
+    asm("{\n\t.reg .b64 x, y, m;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "mov.b64 m, {%4, %4};\n\tfma.rn.f32x2 x, y, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(c), "f"(d), "f"(-1.f));
+}
 // One box into L2 only.
 __device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
                      reinterpret_cast<uint64_t>(tmap)),
                  "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
+}
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -127,10 +165,10 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     const int nchunks = (int)((sl.end - sl.begin + kC - 1) / kC);
     const int j0 = tile * kNV;
 
-    // barriers: each counts the chunks (pairs: one per stage; b_vh: one per half of the rows)
+    // barriers: each counts the chunks (pairs: one per stage, or per buffer of b_vh)
     const uint32_t nb = sb + OFF_BAR;
     const uint32_t b_full = nb, b_qkfree = nb + 16, b_vfree = nb + 32, b_gfull = nb + 48,
-                   b_gfree = nb + 64, b_vh = nb + 80, b_vh0free = nb + 96, b_kv = nb + 104,
+                   b_gfree = nb + 64, b_vh = nb + 80, b_vhfree = nb + 192, b_kv = nb + 104,
                    b_kvfree = nb + 112, b_p = nb + 120, b_pb = nb + 128, b_s = nb + 136,
                    b_sfree = nb + 144, b_o = nb + 152, b_ofree = nb + 160, b_tail = nb + 168,
                    b_vfull = nb + 176;
@@ -144,8 +182,8 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             mbar_init(b_gfull + 8 * i, 1);
             mbar_init(b_gfree + 8 * i, kOut ? 12 : 8);    // one per reading warp
             mbar_init(b_vh + 8 * i, 128);
+            mbar_init(b_vhfree + 8 * i, 1);
         }
-        mbar_init(b_vh0free, 1);
         mbar_init(b_kv, 1);
         mbar_init(b_kvfree, 128);
         mbar_init(b_p, 1);
@@ -159,6 +197,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
+        if (kOut) prefetch_tmap(&maps.o);
     }
     if (warp == 0) {
         tmem_alloc(smem_u32(tmem_s), kTmemCols);
@@ -172,17 +211,11 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     const int row = tid & 127;                               // TMEM lane in warps 0-11
 
     // every lane waits; a warp goes on together or not at all
+    bool failed = false;
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        bool ok = mbar_try_wait(bar, parity & 1u);
-        if (!ok) {
-            const long long t0 = clock64();
-#pragma unroll 1
-            do ok = mbar_try_wait_sleep(bar, parity & 1u);
-            while (!ok && clock64() - t0 <= args.budget);
-        }
-        if (__all_sync(0xffffffffu, ok)) return true;
-        if (lane == 0) set_device_error(p.err, DEV_TIMEOUT);
-        return false;
+        const bool ok = __all_sync(0xffffffffu, wait_phase(bar, parity & 1u, args.budget));
+        failed = !ok;
+        return ok;
     };
     auto rows_of = [&](int c) { return (int)min((long long)kC, sl.end - sl.begin - (long long)c * kC); };
     auto gates = [&](int c) {
@@ -191,59 +224,6 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
 
     if (warp < 4) {
         // ============================================================ scores
-        // o = P V + e^G (Q S) of chunk c: this thread's row, 32 columns at a time. Four lanes
-        // exchange their rows' 16-byte pieces, so that a store covers 64 bytes of each of 8 rows
-        // instead of 16 bytes of each of 32.
-        auto store = [&](int c, float er) {
-            const int valid = rows_of(c), r0 = 32 * warp + (lane & ~3);
-            const bool b0 = lane & 1, b1 = lane & 2;
-            __nv_bfloat16* to =
-                static_cast<__nv_bfloat16*>(p.o) +
-                ((sl.begin + (long long)c * kC + r0) * p.H + h) * (long long)p.dv + j0 +
-                8 * (lane & 3);
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-                uint32_t u[4][4];
-                {
-                    float x[32], y[32];
-                    tmem_ld32(tbase + lq + TM_O1 + 32 * hf, x);
-                    tmem_ld32(tbase + lq + TM_O2 + 64 * (c & 1) + 32 * hf, y);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        u[i / 4][i % 4] = pack2(fmaf(er, y[2 * i], x[2 * i]),
-                                                fmaf(er, y[2 * i + 1], x[2 * i + 1]));
-                }
-                if (hf == 1) {
-                    tc_fence_before();
-                    mbar_arrive(b_ofree);
-                }
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-#pragma unroll
-                    for (int m = 0; m < 4; m += 2) {
-                        const uint32_t got =
-                            __shfl_xor_sync(0xffffffffu, b0 ? u[m][w] : u[m + 1][w], 1);
-                        if (b0) u[m][w] = got;
-                        else u[m + 1][w] = got;
-                    }
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint32_t got =
-                            __shfl_xor_sync(0xffffffffu, b1 ? u[m][w] : u[m + 2][w], 2);
-                        if (b1) u[m][w] = got;
-                        else u[m + 2][w] = got;
-                    }
-                }
-                if (j0 + 32 * hf + 8 * (lane & 3) < p.dv) {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)   // row r0 + m
-                        if (r0 + m < valid)
-                            *reinterpret_cast<uint4*>(to + (long long)m * p.H * p.dv + 32 * hf) =
-                                make_uint4(u[m][0], u[m][1], u[m][2], u[m][3]);
-                }
-            }
-        };
         // chunk c's scores, then, while chunk c + 1's are multiplied, chunk c - 1's output
         const uint32_t pb = tbase + lq + TM_PB;
         float er_last = 0.f;
@@ -312,9 +292,52 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
             }
-            if (c > 0) store(c - 1, er_last);
+            if (c > 0) {   // o = P V + e^G (Q S) of chunk c - 1, staged in shared memory
+                if (tid == 0) bulk_wait_read_all();   // the previous output has left it
+                bar_sync(1, 128);
+                uint8_t* to = sm + OFF_OUT + row * 128;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float x[32], y[32];
+                    tmem_ld32(tbase + lq + TM_O1 + 32 * hf, x);
+                    tmem_ld32(tbase + lq + TM_O2 + 64 * ((c - 1) & 1) + 32 * hf, y);
+                    tmem_ld_wait();
+                    if (hf == 1) {
+                        tc_fence_before();
+                        mbar_arrive(b_ofree);
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        pk[i] = pack2(fmaf(er_last, y[2 * i], x[2 * i]),
+                                      fmaf(er_last, y[2 * i + 1], x[2 * i + 1]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(to + (((4 * hf + i) ^ (row & 7)) << 4)) =
+                            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                }
+                const int valid = rows_of(c - 1);
+                const long long t = sl.begin + (long long)(c - 1) * kC;
+                if (valid == kC) {
+                    fence_proxy_async();
+                    bar_sync(1, 128);
+                    if (tid == 0) {
+                        tma_store_3d(&maps.o, sb + OFF_OUT, j0, h, (int)t);
+                        bulk_commit();
+                    }
+                } else if (row < valid) {   // not the rows behind the sequence's end
+                    __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.o) +
+                                       ((t + row) * p.H + h) * (long long)p.dv + j0;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i)
+                        if (j0 + 8 * i < p.dv)
+                            *reinterpret_cast<uint4*>(g + 8 * i) =
+                                *reinterpret_cast<const uint4*>(to + ((i ^ (row & 7)) << 4));
+                }
+            }
             er_last = er;
         }
+        if (kOut && tid == 0) bulk_wait_read_all();
     } else if (warp < 8) {
         // ============================================================ state
         const size_t unit = (size_t)p.dk * p.dv;
@@ -344,6 +367,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         if (kOut && nchunks > 0) publish();
         float decay = 0.f;   // log of the product over the walk (states only)
         int c = 0;
+#pragma unroll 1
         for (; c < nchunks; ++c) {
             if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
             const float4 tot = *reinterpret_cast<const float4*>(gates(c) + 2 * kC);
@@ -373,7 +397,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         }
         float* out = kOut ? (sl.last && p.hT ? p.hT + ((size_t)sl.n * p.H + h) * unit : nullptr)
                           : p.seg_state + ((size_t)g * p.H + h) * unit;
-        if (out && c == nchunks && row < p.dk) {
+        if (out && !failed && row < p.dk) {
 #pragma unroll
             for (int i = 0; i < kNV; i += 4)
                 if (j0 + i < p.dv)
@@ -383,55 +407,55 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         if (!kOut && tile == 0 && row == 0) p.seg_decay[(size_t)g * p.H + h] = exp2f(decay);
     } else if (warp < 12) {
         // ============================================================ values
-        const int vr = tid & 63, vcol = 4 * (tid >> 6 & 1);   // value row (mod 64), first 16 bytes
+        // 32 rows at a time: lane r takes row r of a quarter, the warp 16 of the columns
+        const int v0 = 2 * (warp & 3);   // first 16-byte piece
 #pragma unroll 1
         for (int c = 0; c < nchunks; ++c) {
             if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
             const float* gt = gates(c);
-            float ek[2];
+            float ek[4], behind = 1.f;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {   // rows vr, 64 + vr
-                float behind = 0.f;
-#pragma unroll
-                for (int m = 1; m < 4; ++m)
-                    if (m > 2 * hf + (vr >> 5)) behind += gt[2 * kC + m];
-                ek[hf] = ex2(behind) * gt[kC + 64 * hf + vr];
+            for (int q = 3; q >= 0; --q) {
+                ek[q] = behind * gt[kC + 32 * q + lane];
+                behind *= ex2(gt[2 * kC + q]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
             if (!wait(b_vfull + 8 * (c & 1), c >> 1)) break;
-            const uint8_t* v = sm + (c & 1) * kStage + ST_V + vr * 128;
-            uint8_t* vh = sm + OFF_VH + vr * 128;
+            const uint8_t* v = sm + (c & 1) * kStage + ST_V + lane * 128;
             bool ok = true;
 #pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-                // a half is free once the previous chunk's product with it is done
-                ok = c == 0 || wait(hf ? b_kv : b_vh0free, c - 1);
+            for (int q = 0; q < 4; ++q) {
+                // a buffer's use u = 2 c + q / 2 follows the product that read use u - 1
+                const int u = 2 * c + (q >> 1);
+                ok = u == 0 || wait(b_vhfree + 8 * (q & 1), u - 1);
                 if (!ok) break;
-                const float f = hf ? ek[1] : ek[0];
-#pragma unroll 2
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t ch = (uint32_t)((vcol + i) ^ (vr & 7)) << 4;
-                    const uint4 u = *reinterpret_cast<const uint4*>(v + hf * (kPanel / 2) + ch);
-                    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+                uint8_t* vh = sm + OFF_VH + (q & 1) * kVH + lane * 128;
+                const float f = ek[0];
+                ek[0] = ek[1], ek[1] = ek[2], ek[2] = ek[3];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t ch = (uint32_t)((v0 + i) ^ (lane & 7)) << 4;
+                    const uint4 x = *reinterpret_cast<const uint4*>(v + q * kQuarter + ch);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                     uint32_t t[3][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float a = f * lo_bf(in[e]), b = f * hi_bf(in[e]);
+                        float a = lo_bf(in[e]), b = hi_bf(in[e]);
+                        mul2(a, b, f);
 #pragma unroll
                         for (int m = 0; m < 3; ++m) {
                             t[m][e] = pack2(a, b);
-                            a -= lo_bf(t[m][e]);
-                            b -= hi_bf(t[m][e]);
+                            if (m < 2) sub2(a, b, lo_bf(t[m][e]), hi_bf(t[m][e]));
                         }
                     }
 #pragma unroll
                     for (int m = 0; m < 3; ++m)
-                        *reinterpret_cast<uint4*>(vh + hf * kHalf + m * (kPanel / 2) + ch) =
+                        *reinterpret_cast<uint4*>(vh + m * kQuarter + ch) =
                             make_uint4(t[m][0], t[m][1], t[m][2], t[m][3]);
                 }
                 fence_proxy_async();
-                mbar_arrive(b_vh + 8 * hf);
+                mbar_arrive(b_vh + 8 * (q & 1));
             }
             if (!ok) break;
         }
@@ -439,43 +463,33 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         // ============================================================ loader
         // Loads of a chunk follow its stage's release, a chunk before their use; its tiles are
         // fetched into L2 two chunks before that, so that they then take an L2 hit's time.
-        const uint32_t qk_bytes = (kOut ? 4u : 2u) * kPanel;
-        auto ahead = [&](int c) {
-            if (c >= nchunks || lane != 0) return;
-            const int t = (int)(sl.begin + (long long)c * kC);
-            tma_prefetch_3d(&maps.k, 0, hk, t);
-            tma_prefetch_3d(&maps.k, 64, hk, t);
-            if (kOut) {
-                tma_prefetch_3d(&maps.q, 0, hk, t);
-                tma_prefetch_3d(&maps.q, 64, hk, t);
-            }
-            tma_prefetch_3d(&maps.v, j0, h, t);
-        };
+        constexpr int kBoxes = kOut ? 4 : 2;   // k's two panels, then q's
+        auto place = [&](int m) { return m < 2 ? ST_K + m * kPanel : ST_Q + (m - 2) * kPanel; };
 #pragma unroll 1
         for (int c = -2; c < nchunks; ++c) {
             const int s = c & 1;
-            ahead(c + 4);
+            if (c + 4 < nchunks && lane == 0) {
+                const int t = (int)(sl.begin + (long long)(c + 4) * kC);
+#pragma unroll 1
+                for (int m = 0; m < kBoxes; ++m)
+                    tma_prefetch_3d(m < 2 ? &maps.k : &maps.q, 64 * (m & 1), hk, t);
+                tma_prefetch_3d(&maps.v, j0, h, t);
+            }
             if (c < 0) continue;
             if (args.debug_stall && !wait(b_tail, 0)) break;
             if (c >= 2 && !wait(b_qkfree + 8 * s, (c >> 1) - 1)) break;
             const int valid = rows_of(c);
             const int t = (int)(sl.begin + (long long)c * kC);
             const uint32_t st = sb + s * kStage;
-            const uint32_t qk_bar = valid < kC ? b_tail : b_full + 8 * s;
             if (lane == 0) {
-                mbar_arrive_expect_tx(qk_bar, qk_bytes + (valid < kC ? kPanel : 0u));
-                tma_load_3d(st + ST_K, &maps.k, qk_bar, 0, hk, t);
-                tma_load_3d(st + ST_K + kPanel, &maps.k, qk_bar, 64, hk, t);
-                if (kOut) {
-                    tma_load_3d(st + ST_Q, &maps.q, qk_bar, 0, hk, t);
-                    tma_load_3d(st + ST_Q + kPanel, &maps.q, qk_bar, 64, hk, t);
-                }
+                const uint32_t bar = valid < kC ? b_tail : b_full + 8 * s;
+                mbar_arrive_expect_tx(bar, (kBoxes + (valid < kC ? 1 : 0)) * kPanel);
+#pragma unroll 1
+                for (int m = 0; m < kBoxes; ++m)
+                    tma_load_3d(st + place(m), m < 2 ? &maps.k : &maps.q, bar, 64 * (m & 1), hk, t);
             }
             __syncwarp();
-            if (c >= 2 && !wait(b_vfree + 8 * s, (c >> 1) - 1)) {
-                // the tail's v never comes: nothing waits for b_tail's phase then
-                break;
-            }
+            if (c >= 2 && !wait(b_vfree + 8 * s, (c >> 1) - 1)) break;
             if (lane == 0) {
                 const uint32_t bar = valid < kC ? b_tail : b_vfull + 8 * s;
                 if (valid == kC) mbar_arrive_expect_tx(bar, kPanel);
@@ -486,7 +500,9 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 if (!wait(b_tail, 0)) break;
                 uint8_t* at = sm + s * kStage + ST_K;   // k's two panels, then v's
                 const int vecs = (kC - valid) * 8;      // 16-byte pieces per panel
+#pragma unroll 1
                 for (int m = 0; m < 3; ++m)
+#pragma unroll 1
                     for (int i = lane; i < vecs; i += 32)
                         *reinterpret_cast<uint4*>(at + m * kPanel + valid * 128 + i * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
@@ -500,52 +516,53 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         }
         // copies in flight land before the shared memory goes away (bounded; a completed phase
         // returns at once)
+#pragma unroll 1
         for (int c = max(0, nchunks - 2); c < nchunks; ++c) {
             const uint32_t par = (uint32_t)((c >> 1) & 1);
             if (rows_of(c) < kC) {
-                mbar_wait(b_tail, 0u, args.budget);
+                wait_phase(b_tail, 0u, args.budget);
             } else {
-                mbar_wait(b_full + 8 * (c & 1), par, args.budget);
-                mbar_wait(b_vfull + 8 * (c & 1), par, args.budget);
+                wait_phase(b_full + 8 * (c & 1), par, args.budget);
+                wait_phase(b_vfull + 8 * (c & 1), par, args.budget);
             }
         }
     } else if (warp == kStateMma) {
         // ============================================================ the state's products
         const uint64_t dM = sw128_desc(0, kPanel, 1024);         // MN-major, 128-row panels
-        const uint64_t dV = sw128_desc(0, kPanel / 2, 1024);     // MN-major, 64-row panels
+        const uint64_t dV = sw128_desc(0, kQuarter, 1024);       // MN-major, 32-row panels
         const uint32_t id2 = idesc_bf16(128, 2 * kNV, 1, 1), id1 = idesc_bf16(128, kNV, 1, 1);
-        // 64 rows: the first two terms side by side, then the third onto the second's sum
-        auto half = [&](uint32_t k, uint32_t v, bool add) {
-#pragma unroll 2
-            for (int s = 0; s < 4; ++s) {
-                umma_f16_warp(tbase + TM_KV, desc_at(dM, k + 2048 * s), desc_at(dV, v + 2048 * s),
-                              id2, add || s > 0);
-                umma_f16_warp(tbase + TM_KV + kNV, desc_at(dM, k + 2048 * s),
-                              desc_at(dV, v + kPanel + 2048 * s), id1, 1);
-            }
-        };
         int c = 0;
         bool ok = true;
 #pragma unroll 1
         for (; c < nchunks; ++c) {
-            const uint32_t k = sb + (c & 1) * kStage + ST_K;
+            uint32_t k = sb + (c & 1) * kStage + ST_K;
             ok = wait(b_full + 8 * (c & 1), c >> 1) && (c == 0 || wait(b_kvfree, c - 1));
 #pragma unroll 1
-            for (int hf = 0; ok && hf < 2; ++hf) {
-                ok = wait(b_vh + 8 * hf, c);
+            for (int q = 0; ok && q < 4; ++q) {
+                ok = wait(b_vh + 8 * (q & 1), 2 * c + (q >> 1));
                 if (!ok) break;
                 tc_fence_after();
-                half(k + hf * (kPanel / 2), sb + OFF_VH + hf * kHalf, hf);
-                umma_commit_warp(hf ? b_kv : b_vh0free);
+                uint32_t v = sb + OFF_VH + (q & 1) * kVH;
+                // the first two terms side by side, then the third onto the second's sum
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    umma_f16_warp(tbase + TM_KV, desc_at(dM, k), desc_at(dV, v), id2, q > 0 || s > 0);
+                    umma_f16_warp(tbase + TM_KV + kNV, desc_at(dM, k), desc_at(dV, v + 2 * kQuarter),
+                                  id1, 1);
+                    k += 2048;
+                    v += 2048;
+                }
+                umma_commit_warp(b_vhfree + 8 * (q & 1));
             }
             if (!ok) break;
+            umma_commit_warp(b_kv);
             umma_commit_warp(b_qkfree + 8 * (c & 1));
             if (!kOut) umma_commit_warp(b_vfree + 8 * (c & 1));
         }
         // every product issued is finished before TMEM and the shared memory go away: the last
         // chunk's, or, on the way out after an expired wait, what this last commit covers
         if (c < nchunks) umma_commit_warp(b_kv);
-        if (nchunks > 0) mbar_wait(b_kv, (uint32_t)(min(c, nchunks - 1) & 1), args.budget);
+        if (nchunks > 0) wait_phase(b_kv, (uint32_t)(min(c, nchunks - 1) & 1), args.budget);
     } else if (warp == kOutMma) {
         // ============================================================ scores, Q S and P V
         const uint64_t dK = sw128_desc(0, 16, 1024);          // K-major
@@ -593,11 +610,11 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         }
         if (kOut && nchunks > 0) {
             if (c < nchunks) umma_commit_warp(b_o);
-            mbar_wait(b_o, (uint32_t)(max(0, min(c, nchunks - 1)) & 1), args.budget);
+            wait_phase(b_o, (uint32_t)(max(0, min(c, nchunks - 1)) & 1), args.budget);
         }
     } else {
         // ============================================================ gates
-        float x[4], nx[4];
+        float x[4], nx[4] = {0.f, 0.f, 0.f, 0.f};
         auto fetch = [&](int c, float (&to)[4]) {
             const int valid = c < nchunks ? rows_of(c) : 0;
             const long long t = sl.begin + (long long)c * kC + 4 * lane;
@@ -608,9 +625,12 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 to[e] = 1.4426950408889634f * (y < -110.f ? -110.f : y);   // in powers of two
             }
         };
-        fetch(0, x);
-        for (int c = 0; c < nchunks; ++c) {
+#pragma unroll 1
+        for (int c = -1; c < nchunks; ++c) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = nx[e];
             fetch(c + 1, nx);
+            if (c < 0) continue;
             if (c >= 2 && !wait(b_gfree + 8 * (c & 1), (c >> 1) - 1)) break;
             float* gt = gates(c);
             // inclusive prefix and exclusive suffix sums in the lane's 32-row block (8 lanes)
@@ -635,20 +655,19 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             if ((lane & 7) == 0) gt[2 * kC + (lane >> 3)] = down;
             __syncwarp();
             if (lane == 0) mbar_arrive(b_gfull + 8 * (c & 1));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = nx[e];
         }
     }
+    if (failed && lane == 0) set_device_error(p.err, DEV_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tbase, kTmemCols);
 }
 
-long long wait_budget() {
-    static const long long budget = [] {
+uint32_t wait_budget() {
+    static const uint32_t budget = [] {
         const char* s = std::getenv("KDA_DEBUG_WAIT_CYCLES");
         const long long v = s && *s ? std::atoll(s) : 0;
-        return v > 0 ? v : 1ll << 31;   // about one second of SM clock
+        return v > 0 && v < 1ll << 31 ? (uint32_t)v : 1u << 31;   // about one second of SM clock
     }();
     return budget;
 }
@@ -690,7 +709,8 @@ cudaError_t launch_linear_chunk(const LinearParams& p, LinearPass pass, cudaStre
     };
     if ((e = map(&m.q, p.q, p.Hk, p.dk)) != cudaSuccess ||
         (e = map(&m.k, p.k, p.Hk, p.dk)) != cudaSuccess ||
-        (e = map(&m.v, p.v, p.H, p.dv)) != cudaSuccess)
+        (e = map(&m.v, p.v, p.H, p.dv)) != cudaSuccess ||
+        (e = map(&m.o, p.o, p.H, p.dv)) != cudaSuccess)
         return e;
     if (pass == LinearPass::kStates)
         linear_chunk_kernel<false><<<(unsigned)blocks, kThreads, kSmem, stream>>>(m, a);
