@@ -154,6 +154,10 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _dev(t, name, dtype=None, shape=None, device=None):
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape) and (device is None or t.device == device)
+            and t.is_contiguous()):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device.type != "cuda":
@@ -551,6 +555,34 @@ def decode_tokens(q, k, v, log_g, beta, S, *, o=None, stream=None):
     return o
 
 
+class _Current:
+    """Stands for ``torch.cuda.device(device)`` where that device is the current one already."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        return False
+
+
+_CURRENT = _Current()
+
+
+def _device(device):
+    return _CURRENT if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+
+
+def _handle(stream, device):
+    """Raw handle of `stream`, or of the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _on(stream):
     """Allocate for work on `stream`: a tensor made here comes from that stream's memory, so that
     nothing pending on the current stream still uses it and its reuse follows the call."""
@@ -628,10 +660,10 @@ def linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, *, output_final_state: 
     else:
         _dev(workspace, "workspace", torch.uint8, None, dev)
     ws_bytes = 0 if workspace is None else workspace.numel()
-    with torch.cuda.device(dev):
-        st = lib().kda_linear_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_g),
-                                  _ptr(h0), _ptr(cu_seqlens), _ptr(o), _ptr(hT), _ptr(workspace),
-                                  ws_bytes, _stream(stream, dev))
+    with _device(dev):
+        st = lib().kda_linear_fwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(log_g),
+                                  _at(h0), _at(cu_seqlens), _at(o), _at(hT), _at(workspace),
+                                  ws_bytes, _handle(stream, dev))
     _check(st, "kda_linear_fwd")
     return o, hT
 
@@ -662,9 +694,9 @@ def linear_decode(q, k, v, log_g, S, *, o=None, stream=None):
             o = torch.empty(tuple(v.shape), dtype=dt, device=dev)
     else:
         _dev(o, "o", dt, tuple(v.shape), dev)
-    with torch.cuda.device(dev):
-        st = lib().kda_linear_decode(N, T, H, Hk, dk, dv, _dtype_code(q), gate, _ptr(q), _ptr(k),
-                                     _ptr(v), _ptr(log_g), _ptr(S), _ptr(o), _stream(stream, dev))
+    with _device(dev):
+        st = lib().kda_linear_decode(N, T, H, Hk, dk, dv, _dtype_code(q), gate, _at(q), _at(k),
+                                     _at(v), _at(log_g), _at(S), _at(o), _handle(stream, dev))
     _check(st, "kda_linear_decode")
     return o
 
@@ -705,10 +737,10 @@ def decode_tree(q, k, v, log_g, beta, parents, S, *, o=None, stream=None):
             o = torch.zeros(tuple(k.shape), dtype=dt, device=dev)
     else:
         _dev(o, "o", dt, tuple(k.shape), dev)
-    with torch.cuda.device(dev):
-        st = lib().kda_decode_tree(N, H, T, _dtype_code(k), _ptr(q), _ptr(k), _ptr(v),
-                                   _ptr(log_g), _ptr(beta), _ptr(parents), _ptr(S), _ptr(o),
-                                   _stream(stream, dev))
+    with _device(dev):
+        st = lib().kda_decode_tree(N, H, T, _dtype_code(k), _at(q), _at(k), _at(v),
+                                   _at(log_g), _at(beta), _at(parents), _at(S), _at(o),
+                                   _handle(stream, dev))
     _check(st, "kda_decode_tree")
     return o
 
@@ -721,10 +753,10 @@ def commit_path(k, v, log_g, beta, path, S, *, stream=None):
     _dev(path, "path", torch.int32, None, dev)
     if path.dim() != 2 or path.shape[0] != N:
         raise ValueError("path must be [N, A]")
-    with torch.cuda.device(dev):
-        st = lib().kda_commit_path(N, H, T, path.shape[1], _dtype_code(k), _ptr(k), _ptr(v),
-                                   _ptr(log_g), _ptr(beta), _ptr(path), _ptr(S),
-                                   _stream(stream, dev))
+    with _device(dev):
+        st = lib().kda_commit_path(N, H, T, path.shape[1], _dtype_code(k), _at(k), _at(v),
+                                   _at(log_g), _at(beta), _at(path), _at(S),
+                                   _handle(stream, dev))
     _check(st, "kda_commit_path")
 
 
@@ -749,9 +781,9 @@ def state_copy(S, src, dst, *, page_dim: int = 0, stream=None):
     page = S.element_size()
     for x in S.shape[page_dim + 1:]:
         page *= x
-    with torch.cuda.device(dev):
-        st = lib().kda_state_copy(_ptr(S), layers, S.shape[page_dim], page, _ptr(src), _ptr(dst),
-                                  src.numel(), _stream(stream, dev))
+    with _device(dev):
+        st = lib().kda_state_copy(_at(S), layers, S.shape[page_dim], page, _at(src), _at(dst),
+                                  src.numel(), _handle(stream, dev))
     _check(st, "kda_state_copy")
 
 

@@ -947,10 +947,12 @@ kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_
         return fail(KDA_ERR_INVALID_ARG, "S_inout overlaps another argument");
     kda::LinearParams p = linear_params(&d);
     p.q = q; p.k = k; p.v = v; p.log_g = log_g; p.o = o;
-    p.h0 = p.hT = S_inout;   // each warp reads its own block of S before it writes it
+    p.h0 = p.hT = S_inout;   // each thread writes what it alone has read
     if ((st = device_error_word(&p.err)) != KDA_OK) return st;
-    const cudaError_t e = kda::launch_linear_walk(p, kda::LinearPass::kWhole,
-                                                  reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = kda::linear_decode_takes(T, dk, dv)
+                              ? kda::launch_linear_decode(p, s)
+                              : kda::launch_linear_walk(p, kda::LinearPass::kWhole, s);
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_linear_decode launch");
 }
 

@@ -101,6 +101,9 @@ cudaError_t launch_linear_walk(const LinearParams& p, LinearPass pass, cudaStrea
 constexpr int kLinearChunk = 128;
 bool linear_chunk_takes(bool bf16, int dk, int dv);
 cudaError_t launch_linear_chunk(const LinearParams& p, LinearPass pass, cudaStream_t stream);
+// A few tokens of whole sequences in place (state at hT): registers hold the state.
+bool linear_decode_takes(int T, int dk, int dv);
+cudaError_t launch_linear_decode(const LinearParams& p, cudaStream_t stream);
 // Chains the segments' initial states: seg_state[n, s] <- state before segment s >= 1.
 cudaError_t launch_linear_combine(const LinearParams& p, cudaStream_t stream);
 // Sets the error word where cu_seqlens does not rise from 0 to T (segmented launches may not
