@@ -10,21 +10,23 @@
 // node) follows the tree's order. A path's rows are a tree without branches, and the state after
 // its last row e is diag(d_e) S + sum_j (d_ej k_j) u_j^T.
 //
-// One 256-thread block per (sequence, head); two blocks fit an SM. Phases:
-//   load     warp w issues the loads of value columns [16 w, 16 w + 16) of S straight into the
-//            registers that the products below read (64 per thread, all in flight at once); the
-//            rows of k and the gates go to shared memory.
-//   walk     a warp per node i walks i's ancestors with d_ij in registers (4 channels per lane):
-//            only products of gates <= 1 appear, so no gate, -inf included, is out of range. It
-//            leaves the two scalars per pair and the rows k_i d_i, q_i d_i.
+// The tree: one block of 256 threads per (sequence, head), two per SM, up to 32 nodes (512 threads,
+// one per SM, above). Phases:
+//   load     S by bulk copies of its rows into shared memory, under way until the product; the
+//            rows of k and the gates.
+//   walk     a warp per node i walks i's ancestors, four at a time, with d_ij in registers (4
+//            channels per lane): only products of gates <= 1 appear, so no gate, -inf included,
+//            is out of range. It leaves the two scalars of each pair and the rows k_i d_i, q_i d_i.
 //   product  [k d; q d] S on the tensor cores (warp-level tf32 products: 16 x 8 x 8). The tree of
-//            bf16 rows uses one tf32 product (its operands lose at most 2^-11, below the bf16
-//            output's 2^-8); fp32 rows, and the commit, whose state stays fp32, split both
-//            operands into a tf32 part and a tf32 remainder and sum three products (2^-21).
-//   solve    a thread per value column substitutes forward through the nodes, 16 at a time in
-//            registers, and writes o.
-//   update   (commit) S = d_e S + sum_j (d_ej k_j) u_j^T in the same registers, then stored.
+//            bf16 rows uses one tf32 product (its operands lose at most 2^-11 and 2^-10, below the
+//            bf16 output's 2^-8); fp32 rows split both operands into a tf32 part and a tf32
+//            remainder and sum three products (2^-21).
+//   solve    a thread per value column and block of 16 nodes substitutes forward in registers:
+//            each u, once known, leaves all later rows' sums, so that a step waits for one
+//            product only; then the blocks behind take the block's u from shared memory.
 // Bound: HBM (64 KiB of state per block, twice for the commit).
+
+#include <algorithm>
 
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
@@ -32,16 +34,16 @@
 namespace kda {
 namespace {
 
-using sm100::mma_tf32_16x8x8;
+using namespace sm100;
 
 constexpr int kD = 128;
-constexpr int kThreads = 256;
-constexpr int kWarps = 8;
-constexpr int kFrag = 132;   // floats per (16 rows, 8 channels) block of the left operand, padded:
-                             // consecutive blocks start four banks apart
-constexpr int kXs = 144;     // floats per row of the products: two rows' 16-byte stores per
-                             // quarter warp fall in different banks
-constexpr int kPh = 36;      // floats per row phase of the update's keys, padded
+// Threads of a tree's block: one per value column and block of nodes in the solve, 8 warps at least.
+constexpr int tree_threads(int nb) { return nb > 2 ? 512 : 256; }
+constexpr int kB = 16;       // nodes per block of the solve
+constexpr int kLd = 136;     // floats per state row in shared memory: a fragment's four rows start
+                             // 8 banks apart, so that half a warp's 8-byte loads do not collide
+constexpr uint32_t kStateBytes = kD * kD * 4;
+constexpr uint32_t kWaitCycles = 1u << 31;   // about one second
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -61,114 +63,134 @@ __device__ __forceinline__ uint32_t tf32_rn(float x) {
     return r;
 }
 
-// Sums of a and b over the warp, in every lane.
-__device__ __forceinline__ void warp_sum2(float& a, float& b, int lane) {
-    const bool up = lane & 16;
-    float x = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+// Sum of x[i] over the warp's lanes; lane l returns the sum of x[l / 4].
+__device__ __forceinline__ float warp_sum8(const float (&x)[8], int lane) {
+    float y[4], z[2], w;
+    const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    const float y = __shfl_xor_sync(0xffffffffu, x, 16);
-    a = up ? y : x;
-    b = up ? x : y;
-}
-
-// Row m of the left operand, channels 4 lane .. 4 lane + 3, into fragment order (rows g, g + 8 and
-// channels t, t + 4 of lane 4 g + t).
-__device__ __forceinline__ void store_frag(float* frag, int m, int lane, float4 x) {
-    const int r = m & 15;
-    float* p = frag + ((m >> 4) * 16 + (lane >> 1)) * kFrag + (r & 7) * 16 + (r >> 3) +
-               2 * (lane & 1);
-    p[0] = x.x;
-    p[4] = x.y;
-    p[8] = x.z;
-    p[12] = x.w;
-}
-
-// S columns [16 warp, +16): this thread's rows 8 s + t and 8 s + t + 4 at [2 s] and [2 s + 1],
-// columns 2 g and 2 g + 1 (the first and second 8-column tile of the product).
-__device__ __forceinline__ void load_state(float2 (&s)[32], const float* S, int warp, int lane) {
-    const float* p = S + (size_t)(lane & 3) * kD + 16 * warp + 2 * (lane >> 2);
+    for (int i = 0; i < 4; ++i)
+        y[i] = (b4 ? x[4 + i] : x[i]) + __shfl_xor_sync(0xffffffffu, b4 ? x[i] : x[4 + i], 16);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        s[i] = __ldcs(reinterpret_cast<const float2*>(p + (size_t)(4 * i) * kD));
+    for (int i = 0; i < 2; ++i)
+        z[i] = (b3 ? y[2 + i] : y[i]) + __shfl_xor_sync(0xffffffffu, b3 ? y[i] : y[2 + i], 8);
+    w = (b2 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, b2 ? z[0] : z[1], 4);
+    w += __shfl_xor_sync(0xffffffffu, w, 2);
+    w += __shfl_xor_sync(0xffffffffu, w, 1);
+    return w;
 }
 
-// Rows [16 mt, +16) of the product with S into x (stride kXs).
+// Row r (of 16) of a tile of the left operand, channels 4 lane .. 4 lane + 3, into fragment order:
+// per 8 channels 128 floats, lane 4 g + t's four values (rows g, g + 8, channels t, t + 4) together,
+// the lanes' places permuted by the channel block so that the blocks' stores fall in different
+// banks.
+template <bool kRound>   // to tf32, for the plain product
+__device__ __forceinline__ void store_frag(float* tile, int r, int lane, float4 x) {
+    if (kRound)
+        x = make_float4(__uint_as_float(tf32_rn(x.x)), __uint_as_float(tf32_rn(x.y)),
+                        __uint_as_float(tf32_rn(x.z)), __uint_as_float(tf32_rn(x.w)));
+    const int ks = lane >> 1, sw = ks & 7;
+    float* p = tile + ks * 128 + (r >> 3) + 2 * (lane & 1);
+    const int l0 = (r & 7) * 4;
+    p[4 * ((l0 + 0) ^ sw)] = x.x;
+    p[4 * ((l0 + 1) ^ sw)] = x.y;
+    p[4 * ((l0 + 2) ^ sw)] = x.z;
+    p[4 * ((l0 + 3) ^ sw)] = x.w;
+}
+__device__ __forceinline__ float4 load_frag(const float* tile, int ks, int lane) {
+    return load4(tile + ks * 128 + 4 * (lane ^ (ks & 7)));
+}
+
+// acc += one 16-row tile (fragments a) times 16 columns of the state (this lane's rows t and
+// t + 4 of 8, columns 2 g and 2 g + 1: one per 8-column product).
+// Without kSplit the fragments are tf32 values already, and the state's low bits, which the
+// product does not read, are cut off (2^-10 of an element at most).
 template <bool kSplit>
-__device__ __forceinline__ void product(const float2 (&s)[32], const float* frag, float* x, int mt,
-                                        int warp, int lane) {
-    float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int ks = 0; ks < 16; ++ks) {
-        const float4 f = *reinterpret_cast<const float4*>(frag + (mt * 16 + ks) * kFrag + 4 * lane);
-        const uint32_t ah[4] = {tf32_rn(f.x), tf32_rn(f.y), tf32_rn(f.z), tf32_rn(f.w)};
-        const float2 p = s[2 * ks], q = s[2 * ks + 1];
-        const uint32_t b0[2] = {tf32_rn(p.x), tf32_rn(q.x)}, b1[2] = {tf32_rn(p.y), tf32_rn(q.y)};
-        if (kSplit) {
-            const uint32_t al[4] = {tf32_rn(f.x - __uint_as_float(ah[0])),
-                                    tf32_rn(f.y - __uint_as_float(ah[1])),
-                                    tf32_rn(f.z - __uint_as_float(ah[2])),
-                                    tf32_rn(f.w - __uint_as_float(ah[3]))};
-            const uint32_t l0[2] = {tf32_rn(p.x - __uint_as_float(b0[0])),
-                                    tf32_rn(q.x - __uint_as_float(b0[1]))};
-            const uint32_t l1[2] = {tf32_rn(p.y - __uint_as_float(b1[0])),
-                                    tf32_rn(q.y - __uint_as_float(b1[1]))};
-            mma_tf32_16x8x8(a0, al, b0);
-            mma_tf32_16x8x8(a1, al, b1);
-            mma_tf32_16x8x8(a0, ah, l0);
-            mma_tf32_16x8x8(a1, ah, l1);
-        }
-        mma_tf32_16x8x8(a0, ah, b0);
-        mma_tf32_16x8x8(a1, ah, b1);
+__device__ __forceinline__ void mma_step(float (&c0)[4], float (&c1)[4], float4 f, float2 p,
+                                         float2 q) {
+    if (!kSplit) {
+        const uint32_t a[4] = {__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z),
+                               __float_as_uint(f.w)};
+        const uint32_t b0[2] = {__float_as_uint(p.x), __float_as_uint(q.x)};
+        const uint32_t b1[2] = {__float_as_uint(p.y), __float_as_uint(q.y)};
+        mma_tf32_16x8x8(c0, a, b0);
+        mma_tf32_16x8x8(c1, a, b1);
+        return;
     }
-    float* p = x + (size_t)(16 * mt + (lane >> 2)) * kXs + 16 * warp + 4 * (lane & 3);
-    *reinterpret_cast<float4*>(p) = make_float4(a0[0], a1[0], a0[1], a1[1]);
-    *reinterpret_cast<float4*>(p + 8 * kXs) = make_float4(a0[2], a1[2], a0[3], a1[3]);
+    const uint32_t ah[4] = {tf32_rn(f.x), tf32_rn(f.y), tf32_rn(f.z), tf32_rn(f.w)};
+    const uint32_t b0[2] = {tf32_rn(p.x), tf32_rn(q.x)}, b1[2] = {tf32_rn(p.y), tf32_rn(q.y)};
+    const uint32_t al[4] = {
+        tf32_rn(f.x - __uint_as_float(ah[0])), tf32_rn(f.y - __uint_as_float(ah[1])),
+        tf32_rn(f.z - __uint_as_float(ah[2])), tf32_rn(f.w - __uint_as_float(ah[3]))};
+    const uint32_t l0[2] = {tf32_rn(p.x - __uint_as_float(b0[0])),
+                            tf32_rn(q.x - __uint_as_float(b0[1]))};
+    const uint32_t l1[2] = {tf32_rn(p.y - __uint_as_float(b1[0])),
+                            tf32_rn(q.y - __uint_as_float(b1[1]))};
+    mma_tf32_16x8x8(c0, al, b0);
+    mma_tf32_16x8x8(c1, al, b1);
+    mma_tf32_16x8x8(c0, ah, l0);
+    mma_tf32_16x8x8(c1, ah, l1);
+    mma_tf32_16x8x8(c0, ah, b0);
+    mma_tf32_16x8x8(c1, ah, b1);
+}
+__device__ __forceinline__ const float* state_frag(const float* S, int ks, int cols, int lane) {
+    return S + (8 * ks + (lane & 3)) * kLd + cols + 2 * (lane >> 2);
+}
+// A tile's product to rows 0 .. 15 of x, columns cols .. cols + 15.
+__device__ __forceinline__ void store_tile(float* x, int cols, int lane, const float (&c0)[4],
+                                           const float (&c1)[4]) {
+    float* p = x + (lane >> 2) * kLd + cols + 4 * (lane & 3);
+    *reinterpret_cast<float4*>(p) = make_float4(c0[0], c1[0], c0[1], c1[1]);
+    *reinterpret_cast<float4*>(p + 8 * kLd) = make_float4(c0[2], c1[2], c0[3], c1[3]);
 }
 
-// Shared memory of the tree, in floats, for Tp = 16 ceil(T / 16) nodes: the left operand; then k
-// and the gates, whose place the products take; then the two matrices of pairs.
+// Warp 0: the state's rows into shared memory.
+__device__ __forceinline__ void fetch_state(float* s, const float* S, uint32_t bar, int lane) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, kStateBytes);
+    __syncwarp();
+    for (int r = lane; r < kD; r += 32)
+        bulk_load(smem_u32(s + r * kLd), S + (size_t)r * kD, kD * 4, bar);
+}
+
+// NB: blocks of 16 nodes.
+template <typename Tin, int NB>
 struct TreeSmem {
-    int frag, rows, pairs, total;
-    __host__ __device__ explicit TreeSmem(int Tp) {
-        frag = 0;
-        rows = frag + 2 * Tp * kFrag;                 // 2 Tp / 16 row blocks of 16 channel blocks
-        const int in = 2 * Tp * kD, out = 2 * Tp * kXs;
-        pairs = rows + (in > out ? in : out);
-        total = pairs + 2 * Tp * Tp;
-    }
+    static constexpr int kN = kB * NB;
+    float state[kD * kLd];               // S, then the products: rows i of k d S, rows kN + i of q d S
+    float rows[2 * kN * kD];             // k and the gates, then the left operand's fragments
+    float akk[kN * kN], aqk[kN * kN];    // [j][i]: pairs of node i and j above it (and j = i)
+    float u[NB > 1 ? kB * kD : 4];       // the block of u that the blocks behind take
+    unsigned long long bad[NB > 1 ? kD : 1];
+    unsigned long long above[kN];        // the nodes above each node
+    int par[kN];
+    float beta[kN];
+    unsigned long long bar;
+    int bad_tree;
 };
 
-// Two blocks per SM for bf16 rows; the split products of fp32 rows need the registers of one.
-template <typename Tin>
-__global__ void __launch_bounds__(kThreads, sizeof(Tin) == 2 ? 2 : 1)
+template <typename Tin, int NB>
+__global__ void __launch_bounds__(tree_threads(NB), NB <= 2 && sizeof(Tin) == 2 ? 2 : 1)
 decode_tree_kernel(const TreeParams p) {
-    extern __shared__ __align__(16) float sm[];
-    __shared__ int s_par[kMaxTreeNodes];
-    __shared__ float s_beta[kMaxTreeNodes];
-    __shared__ unsigned long long s_above[kMaxTreeNodes];   // the ancestors of each node
-    __shared__ int s_bad;
+    using Smem = TreeSmem<Tin, NB>;
+    constexpr int kN = Smem::kN, kThreads = tree_threads(NB), kWarps = kThreads / 32;
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int unit = blockIdx.x, n = unit / p.H, h = unit % p.H;
-    const int T = p.T, Tp = (T + 15) & ~15;
-    const TreeSmem L(Tp);
-    float *frag = sm + L.frag, *s_k = sm + L.rows, *s_g = s_k + Tp * kD, *x = sm + L.rows;
-    float *akk = sm + L.pairs, *aqk = akk + Tp * Tp;
+    const int unit = blockIdx.x, n = unit / p.H, h = unit % p.H, T = p.T;
+    float *s_k = sm.rows, *s_g = sm.rows + kN * kD;
     const Tin* q = static_cast<const Tin*>(p.q);
     const Tin* k = static_cast<const Tin*>(p.k);
     const Tin* v = static_cast<const Tin*>(p.v);
     auto row = [&](int i) { return (((size_t)n * T + i) * p.H + h) * kD; };
+    const uint32_t bar = smem_u32(&sm.bar);
 
-    float2 s[32];
-    load_state(s, p.S + (size_t)unit * kD * kD, warp, lane);
-
-    if (tid == 0) s_bad = 0;
-    if (tid < kMaxTreeNodes) {
-        const int par = tid < T ? p.nodes[(size_t)n * T + tid] : -2;
-        s_par[tid] = par;
-        s_beta[tid] = par == -2 ? 0.f
-                                : load_elem(static_cast<const Tin*>(p.beta),
-                                            ((int64_t)n * T + tid) * p.H + h);
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_init(bar, 1);
+            fence_mbar_init();
+            sm.bad_tree = 0;
+        }
+        __syncwarp();
+        fetch_state(sm.state, p.S + (size_t)unit * kD * kD, bar, lane);
     }
     for (int i = tid; i < T * (kD / 4); i += kThreads) {
         const int r = i >> 5, c = 4 * (i & 31);
@@ -177,265 +199,437 @@ decode_tree_kernel(const TreeParams p) {
         *reinterpret_cast<float4*>(s_g + r * kD + c) =
             make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
     }
-    for (int i = tid; i < 2 * Tp * Tp / 4; i += kThreads)
-        *reinterpret_cast<float4*>(akk + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < kN) {
+        const int par = tid < T ? p.nodes[(size_t)n * T + tid] : -2;
+        sm.par[tid] = par;
+        sm.beta[tid] = par == -2 ? 0.f
+                                 : load_elem(static_cast<const Tin*>(p.beta),
+                                             ((int64_t)n * T + tid) * p.H + h);
+    }
+    for (int i = tid; i < kN * kN / 2; i += kThreads)   // both matrices
+        *reinterpret_cast<float4*>(sm.akk + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
     if (tid < T) {   // -2: no node; else the root or an earlier node that is there
-        const int par = s_par[tid];
-        if (par < -2 || par >= tid || (par >= 0 && s_par[par] == -2)) s_bad = 1;
+        const int par = sm.par[tid];
+        if (par < -2 || par >= tid || (par >= 0 && sm.par[par] == -2)) sm.bad_tree = 1;
     }
     __syncthreads();
-    if (s_bad) {
-        if (tid == 0) set_device_error(p.err, DEV_BAD_INDEX);
+    if (sm.bad_tree) {   // (the copy lands before its shared memory goes away)
+        if (tid == 0) {
+            set_device_error(p.err, DEV_BAD_INDEX);
+            mbar_wait(bar, 0, kWaitCycles);
+        }
         return;
     }
 
-    for (int i = warp; i < Tp; i += kWarps) {
-        float4 ki = make_float4(0.f, 0.f, 0.f, 0.f), qi = ki, d = ki;
+    // walk: nodes warp, warp + kWarps, ...; their rows stay in registers until every warp has read
+    // k and the gates
+    constexpr int kMine = kN / kWarps;
+    float4 kd[kMine], qd[kMine];
+#pragma unroll
+    for (int b = 0; b < kMine; ++b) {
+        const int i = kWarps * b + warp;
+        kd[b] = qd[b] = make_float4(0.f, 0.f, 0.f, 0.f);
         unsigned long long above = 0;
-        if (s_par[i] != -2) {
-            ki = *reinterpret_cast<const float4*>(s_k + i * kD + 4 * lane);
-            qi = load4(q + row(i) + 4 * lane);
-            float qk = dot4(qi, ki), none = 0.f;
-            warp_sum2(qk, none, lane);
-            if (lane == 0) aqk[i * Tp + i] = qk;
-            d = *reinterpret_cast<const float4*>(s_g + i * kD + 4 * lane);
-            for (int j = s_par[i]; j >= 0; j = s_par[j]) {
-                const float4 kj =
-                    mul4(d, *reinterpret_cast<const float4*>(s_k + j * kD + 4 * lane));
-                float a = dot4(ki, kj), b = dot4(qi, kj);
-                warp_sum2(a, b, lane);
-                if (lane == 0) akk[i * Tp + j] = a, aqk[i * Tp + j] = b;
-                above |= 1ull << j;
-                d = mul4(d, *reinterpret_cast<const float4*>(s_g + j * kD + 4 * lane));
+        if (sm.par[i] != -2) {
+            const float4 ki = load4(s_k + i * kD + 4 * lane), qi = load4(q + row(i) + 4 * lane);
+            float4 d = make_float4(1.f, 1.f, 1.f, 1.f);
+            int j = i;
+#pragma unroll 1
+            while (j >= 0) {
+                float x[8];
+                int at[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    at[m] = j;
+                    x[m] = x[4 + m] = 0.f;
+                    if (j >= 0) {
+                        const float4 kj = mul4(d, load4(s_k + j * kD + 4 * lane));
+                        x[m] = dot4(ki, kj);
+                        x[4 + m] = dot4(qi, kj);
+                        d = mul4(d, load4(s_g + j * kD + 4 * lane));
+                        above |= 1ull << j;
+                        j = sm.par[j];
+                    }
+                }
+                const float sum = warp_sum8(x, lane);
+                const int m = lane >> 2 & 3;
+                const int to = m == 0 ? at[0] : m == 1 ? at[1] : m == 2 ? at[2] : at[3];
+                if ((lane & 3) == 0 && to >= 0) {
+                    if (lane < 16) sm.akk[to * kN + i] = to == i ? 0.f : sum;
+                    else sm.aqk[to * kN + i] = sum;
+                }
             }
+            kd[b] = mul4(ki, d);
+            qd[b] = mul4(qi, d);
         }
-        if (lane == 0) s_above[i] = above;
-        store_frag(frag, i, lane, mul4(ki, d));
-        store_frag(frag, Tp + i, lane, mul4(qi, d));
+        if (lane == 0) sm.above[i] = above & ~(1ull << i);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < kMine; ++b) {
+        const int i = kWarps * b + warp;
+        store_frag<sizeof(Tin) == 2>(sm.rows + (i >> 4) * 2048, i & 15, lane, kd[b]);
+        store_frag<sizeof(Tin) == 2>(sm.rows + (NB + (i >> 4)) * 2048, i & 15, lane, qd[b]);
+    }
+    const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and block of nodes
+    float y[kB], r[kB];
+    if (blk < NB) {
+        const Tin* at = v + row(kB * blk) + col;
+        const size_t step = (size_t)p.H * kD;
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+            r[i] = 0.f;
+            if (sm.par[kB * blk + i] != -2) r[i] = load_elem(at, i * step);
+        }
+    }
+    const bool ok = mbar_wait(bar, 0, kWaitCycles);
+    if (!ok) set_device_error(p.err, DEV_TIMEOUT);
+    if (__syncthreads_or(!ok)) return;
+
+    {   // product: 16 columns per warp; all 2 NB tiles, or k d and q d by 8 warps each
+        constexpr int kTiles = 2 * NB / (kWarps / 8);
+        const int cols = 16 * (warp & 7), t0 = (warp >> 3) * kTiles;
+        const float* frag = sm.rows + t0 * 2048;
+        float c0[kTiles][4], c1[kTiles][4];
+#pragma unroll
+        for (int b = 0; b < kTiles; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c0[b][e] = c1[b][e] = 0.f;
+#pragma unroll 4
+        for (int ks = 0; ks < 16; ++ks) {
+            const float* at = state_frag(sm.state, ks, cols, lane);
+            const float2 s0 = *reinterpret_cast<const float2*>(at);
+            const float2 s1 = *reinterpret_cast<const float2*>(at + 4 * kLd);
+#pragma unroll
+            for (int b = 0; b < kTiles; ++b)
+                mma_step<sizeof(Tin) == 4>(c0[b], c1[b], load_frag(frag + b * 2048, ks, lane), s0, s1);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kTiles; ++b)
+            store_tile(sm.state + kB * (t0 + b) * kLd, cols, lane, c0[b], c1[b]);
     }
     __syncthreads();
 
-    for (int mt = 0; mt < 2 * Tp / 16; ++mt)
-        product<sizeof(Tin) == 4>(s, frag, x, mt, warp, lane);
-    __syncthreads();
-
-    if (tid < kD) {   // a column's rows are read and written by its own thread alone
-        Tin* o = static_cast<Tin*>(p.o);
-        // The pairs of other branches have coefficient 0. An infinite or NaN u would turn that
-        // into NaN, so such a u enters the sums as 0, and `bad` has its node: what is below it
-        // in the tree becomes NaN, what is beside it does not.
-        unsigned long long bad = 0;
-        for (int b = 0; b < Tp; b += 16) {
-            float u[16], vi[16];
+    // The pairs of other branches have coefficient 0. An infinite or NaN u would turn that into
+    // NaN, so such a u enters the sums as 0, and `bad` has its node: what is below it in the tree
+    // becomes NaN, what is beside it does not.
+    unsigned long long bad = 0;
+    Tin* o = static_cast<Tin*>(p.o);
+    if (blk < NB) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                vi[i] = s_par[b + i] != -2 ? load_elem(v, row(b + i) + tid) : 0.f;
+        for (int i = 0; i < kB; ++i) {
+            r[i] -= sm.state[(kB * blk + i) * kLd + col];
+            y[i] = sm.state[(kN + kB * blk + i) * kLd + col];
+        }
+    }
+    for (int b = 0; b < NB; ++b) {
+        if (blk == b) {
+            if (NB > 1 && b > 0) bad = sm.bad[col];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float *ak = akk + (b + i) * Tp, *aq = aqk + (b + i) * Tp;
-                float r = vi[i] - x[(b + i) * kXs + tid], y = x[(Tp + b + i) * kXs + tid];
-                for (int j = 0; j < b; j += 4) {
-                    const float4 a = load4(ak + j), c = load4(aq + j);
-                    const float u0 = x[j * kXs + tid], u1 = x[(j + 1) * kXs + tid],
-                                u2 = x[(j + 2) * kXs + tid], u3 = x[(j + 3) * kXs + tid];
-                    r -= fmaf(a.x, u0, fmaf(a.y, u1, fmaf(a.z, u2, a.w * u3)));
-                    y += fmaf(c.x, u0, fmaf(c.y, u1, fmaf(c.z, u2, c.w * u3)));
+            for (int j = 0; j < kB; ++j) {
+                const int at = kB * b + j;
+                const bool below = bad & sm.above[at];
+                float u = below ? __int_as_float(0x7fc00000) : sm.beta[at] * r[j];
+                const float* ak = sm.akk + at * kN + kB * b;
+                const float* aq = sm.aqk + at * kN + kB * b;
+                y[j] = fmaf(aq[j], u, y[j]);
+                if (!(fabsf(u) <= 3.402823466e38f)) {
+                    u = 0.f;
+                    bad |= 1ull << at;
                 }
 #pragma unroll
-                for (int j = 0; j < i; ++j) {
-                    r = fmaf(-ak[b + j], u[j], r);
-                    y = fmaf(aq[b + j], u[j], y);
+                for (int i4 = 0; i4 < kB; i4 += 4) {
+                    if (i4 + 3 <= j) continue;
+                    const float4 a = load4(ak + i4), c = load4(aq + i4);
+                    const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (i4 + e > j) {
+                            r[i4 + e] = fmaf(-av[e], u, r[i4 + e]);
+                            y[i4 + e] = fmaf(cv[e], u, y[i4 + e]);
+                        }
                 }
-                if (bad & s_above[b + i]) r = y = __int_as_float(0x7fc00000);
-                u[i] = s_beta[b + i] * r;
-                y = fmaf(aq[b + i], u[i], y);
-                if (!(fabsf(u[i]) <= 3.402823466e38f)) {
-                    u[i] = 0.f;
-                    bad |= 1ull << (b + i);
-                }
-                x[(b + i) * kXs + tid] = u[i];
-                if (s_par[b + i] != -2) store_elem(o, row(b + i) + tid, y);
+                if (NB > 1) sm.u[j * kD + col] = u;
+                if (sm.par[at] != -2) store_elem(o, row(at) + col, y[j]);
             }
+            if (NB > 1) sm.bad[col] = bad;
+        }
+        if (NB > 1 && b + 1 < NB) {
+            __syncthreads();
+            if (blk > b && blk < NB) {
+#pragma unroll 4
+                for (int j = 0; j < kB; ++j) {
+                    const float u = sm.u[j * kD + col];
+                    const float* ak = sm.akk + (kB * b + j) * kN + kB * blk;
+                    const float* aq = sm.aqk + (kB * b + j) * kN + kB * blk;
+#pragma unroll
+                    for (int i4 = 0; i4 < kB; i4 += 4) {
+                        const float4 a = load4(ak + i4), c = load4(aq + i4);
+                        const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            r[i4 + e] = fmaf(-av[e], u, r[i4 + e]);
+                            y[i4 + e] = fmaf(cv[e], u, y[i4 + e]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
         }
     }
 }
 
-constexpr int kGroup = 16;   // rows of a path taken at once
+// The commit. One 128-thread block per SM half walks the (sequence, head) units: while it works on
+// one unit's state in registers, the next one's streams into shared memory. Rows are taken four at
+// a time: thread c holds channel c of the rows (their products of gates are its own running
+// products), then, as (row phase, four columns), 32 rows of the state: k d S, the substitution for
+// u in registers, and S = d_e S + sum_j (d_ej k_j) u_j^T, each one pass over the registers of 4 rows'
+// multiply-adds. (Tensor-core products of 16-row tiles, split for fp32, cost more instructions up
+// to about 9 rows: 567 us against 368 us with the state in registers and 512 threads per unit.)
+constexpr int kRows = 4;
+constexpr int kPathThreads = 128;
+struct PathSmem {
+    float state[kD * kD];           // the next unit's state
+    float4 kd[kD], ke[kD];          // [channel][row]: k_j d_j, d_ej k_j
+    float end[kD];                  // d_e
+    float pairs[4][8];              // per warp: pair sums
+    unsigned long long bar;
+};
 
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads, 2)
-commit_path_kernel(const TreeParams p) {
-    __shared__ __align__(16) float frag[16 * kFrag];
-    __shared__ __align__(16) float s_rows[2 * kGroup * kXs];   // k and the gates, then k S
-    __shared__ __align__(16) float s_ke[kGroup][4 * kPh];      // d_ej k_j by row phase
-    __shared__ __align__(16) float s_end[4 * kPh];             // d_e by row phase
-    __shared__ __align__(16) float akk[kGroup * kGroup];
-    __shared__ float s_beta[kGroup];
-    __shared__ int s_row[kGroup];
-    __shared__ int s_len, s_bad;
+__global__ void __launch_bounds__(kPathThreads, 2)
+commit_path_kernel(const TreeParams p, const int units) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    PathSmem& sm = *reinterpret_cast<PathSmem*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int unit = blockIdx.x, n = unit / p.H, h = unit % p.H;
-    const int32_t* path = p.nodes + (size_t)n * p.A;
-    float *s_k = s_rows, *s_g = s_rows + kGroup * kD, *x = s_rows;
+    const int phase = lane >> 3, col = 32 * warp + 4 * (lane & 7);
     const Tin* k = static_cast<const Tin*>(p.k);
     const Tin* v = static_cast<const Tin*>(p.v);
-    auto row = [&](int i) { return (((size_t)n * p.T + i) * p.H + h) * kD; };
+    const uint32_t bar = smem_u32(&sm.bar);
 
-    if (tid == 0) s_len = p.A, s_bad = 0;
-    __syncthreads();
-    for (int i = tid; i < p.A; i += kThreads) {   // the path ends at its first negative entry
-        const int r = path[i];
-        if (r < 0) atomicMin(&s_len, i);
+    // length of a unit's path: up to its first negative entry; -1 where it leaves the rows
+    auto length = [&](int unit) {
+        const int32_t* path = p.nodes + (size_t)(unit / p.H) * p.A;
+        int len = p.A;
+        bool bad = false;
+        for (int i = lane; i - lane < len; i += 32) {   // every warp for itself
+            const int r = i < p.A ? path[i] : -1;
+            const unsigned stop = __ballot_sync(0xffffffffu, r < 0);
+            const int here = stop ? __ffs(stop) - 1 : 32;
+            bad |= lane < here && r >= p.T;
+            if (stop) len = i - lane + here;
+        }
+        return __any_sync(0xffffffffu, bad) ? -1 : len;
+    };
+    // the next unit at or behind u with rows to commit, its length
+    auto next = [&](int u, int* len) {
+        for (; u < units; u += gridDim.x) {
+            *len = length(u);
+            if (*len > 0) break;
+            if (*len < 0 && tid == 0) set_device_error(p.err, DEV_BAD_INDEX);
+        }
+        return u;
+    };
+    auto fetch = [&](int u) {
+        if (tid == 0) {
+            mbar_arrive_expect_tx(bar, kStateBytes);
+            for (int i = 0; i < 4; ++i)
+                bulk_load(smem_u32(sm.state) + i * (kStateBytes / 4),
+                          p.S + (size_t)u * kD * kD + i * (kD * kD / 4), kStateBytes / 4, bar);
+        }
+    };
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
     }
     __syncthreads();
-    const int len = s_len;
-    for (int i = tid; i < len; i += kThreads)
-        if (path[i] >= p.T) s_bad = 1;
-    __syncthreads();
-    if (s_bad) {
-        if (tid == 0) set_device_error(p.err, DEV_BAD_INDEX);
-        return;
-    }
-    if (len == 0) return;
+    int len = 0, unit = next(blockIdx.x, &len);
+    if (unit < units) fetch(unit);
 
-    float2 s[32];
-    float* S = p.S + (size_t)unit * kD * kD;
-    load_state(s, S, warp, lane);
-
-    for (int a0 = 0; a0 < len; a0 += kGroup) {
-        const int m = min(kGroup, len - a0);
-        if (tid < kGroup) {
-            const int r = tid < m ? path[a0 + tid] : 0;
-            s_row[tid] = r;
-            s_beta[tid] =
-                tid < m ? load_elem(static_cast<const Tin*>(p.beta),
-                                    ((int64_t)n * p.T + r) * p.H + h)
-                        : 0.f;
-        }
-        akk[tid] = 0.f;
-        __syncthreads();
-        for (int i = tid; i < m * (kD / 4); i += kThreads) {
-            const int r = i >> 5, c = 4 * (i & 31);
-            const size_t at = row(s_row[r]) + c;
-            const float4 g = load4(p.log_g + at);
-            *reinterpret_cast<float4*>(s_k + r * kD + c) = load4(k + at);
-            *reinterpret_cast<float4*>(s_g + r * kD + c) =
-                make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
-        }
-        __syncthreads();
-
-        for (int i = warp; i < kGroup; i += kWarps) {
-            float4 ki = make_float4(0.f, 0.f, 0.f, 0.f), d = ki;
-            if (i < m) {
-                // channel c sits at row phase c % 4, place 2 (c / 8) + (c / 4) % 2 = c / 4
-                const bool end = i == m - 1;
-                ki = *reinterpret_cast<const float4*>(s_k + i * kD + 4 * lane);
-                d = make_float4(1.f, 1.f, 1.f, 1.f);
-                for (int j = i; j >= 0; --j) {
-                    const float4 kj =
-                        mul4(d, *reinterpret_cast<const float4*>(s_k + j * kD + 4 * lane));
-                    if (end) {
-                        s_ke[j][lane] = kj.x;
-                        s_ke[j][kPh + lane] = kj.y;
-                        s_ke[j][2 * kPh + lane] = kj.z;
-                        s_ke[j][3 * kPh + lane] = kj.w;
-                    }
-                    if (j < i) {
-                        float a = dot4(ki, kj), none = 0.f;
-                        warp_sum2(a, none, lane);
-                        if (lane == 0) akk[i * kGroup + j] = a;
-                    }
-                    d = mul4(d, *reinterpret_cast<const float4*>(s_g + j * kD + 4 * lane));
-                }
-                if (end) {
-                    s_end[lane] = d.x;
-                    s_end[kPh + lane] = d.y;
-                    s_end[2 * kPh + lane] = d.z;
-                    s_end[3 * kPh + lane] = d.w;
+    for (int it = 0; unit < units; ++it) {
+        const int n = unit / p.H, h = unit % p.H;
+        const int32_t* path = p.nodes + (size_t)n * p.A;
+        auto row = [&](int a) { return (((size_t)n * p.T + path[a]) * p.H + h) * kD; };
+        // the first rows' values, while the state lands
+        float kk[kRows], gg[kRows];
+        auto rows = [&](int a0) {
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                kk[j] = 0.f;
+                gg[j] = 1.f;
+                if (a0 + j < len) {
+                    const size_t at = row(a0 + j) + tid;
+                    kk[j] = load_elem(k, at);
+                    gg[j] = expf(p.log_g[at]);
                 }
             }
-            store_frag(frag, i, lane, mul4(ki, d));
-        }
+        };
+        rows(0);
+        const bool ok = mbar_wait(bar, it & 1, kWaitCycles);
+        if (!ok) set_device_error(p.err, DEV_TIMEOUT);
+        if (__syncthreads_or(!ok)) return;
+        float4 s[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = load4(sm.state + (phase + 4 * i) * kD + col);
         __syncthreads();
+        int len_next = 0;
+        const int unit_next = next(unit + gridDim.x, &len_next);
+        if (unit_next < units) fetch(unit_next);
 
-        product<true>(s, frag, x, 0, warp, lane);
-        __syncthreads();
-
-        if (tid < kD) {
-            float u[kGroup], vi[kGroup];
+        for (int a0 = 0; a0 < len; a0 += kRows) {
+            if (a0 > 0) rows(a0);
+            float4 vv[kRows];
+            float beta[kRows];
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-                vi[i] = i < m ? load_elem(v, row(s_row[i]) + tid) : 0.f;
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i) {
-                float r = vi[i] - x[i * kXs + tid];
-#pragma unroll
-                for (int j = 0; j < i; ++j) r = fmaf(-akk[i * kGroup + j], u[j], r);
-                u[i] = s_beta[i] * r;
-                x[i * kXs + tid] = u[i];
+            for (int j = 0; j < kRows; ++j) {
+                vv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                beta[j] = 0.f;
+                if (a0 + j < len) {
+                    vv[j] = load4(v + row(a0 + j) + col);
+                    beta[j] = load_elem(static_cast<const Tin*>(p.beta),
+                                        ((int64_t)n * p.T + path[a0 + j]) * p.H + h);
+                }
             }
-        }
-        __syncthreads();
-
-        const int t = lane & 3, col = 16 * warp + 2 * (lane >> 2);
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 d = load4(s_end + t * kPh + i);
-            s[i].x *= d.x, s[i].y *= d.x;
-            s[i + 1].x *= d.y, s[i + 1].y *= d.y;
-            s[i + 2].x *= d.z, s[i + 2].y *= d.z;
-            s[i + 3].x *= d.w, s[i + 3].y *= d.w;
-        }
-        for (int j = 0; j < m; ++j) {
-            const float2 u = *reinterpret_cast<const float2*>(x + j * kXs + col);
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 c = load4(&s_ke[j][t * kPh + i]);
-                s[i].x = fmaf(c.x, u.x, s[i].x), s[i].y = fmaf(c.x, u.y, s[i].y);
-                s[i + 1].x = fmaf(c.y, u.x, s[i + 1].x), s[i + 1].y = fmaf(c.y, u.y, s[i + 1].y);
-                s[i + 2].x = fmaf(c.z, u.x, s[i + 2].x), s[i + 2].y = fmaf(c.z, u.y, s[i + 2].y);
-                s[i + 3].x = fmaf(c.w, u.x, s[i + 3].x), s[i + 3].y = fmaf(c.w, u.y, s[i + 3].y);
+            // channel tid: products of gates up to each row, from behind each row, between rows
+            const float p0 = gg[0], p1 = p0 * gg[1], p2 = p1 * gg[2], p3 = p2 * gg[3];
+            const float q2 = gg[3], q1 = gg[2] * q2, q0 = gg[1] * q1;
+            sm.kd[tid] = make_float4(kk[0] * p0, kk[1] * p1, kk[2] * p2, kk[3] * p3);
+            sm.ke[tid] = make_float4(kk[0] * q0, kk[1] * q1, kk[2] * q2, kk[3]);
+            sm.end[tid] = p3;
+            {   // pairs (1,0) (2,0) (2,1) (3,0) (3,1) (3,2)
+                const float g12 = gg[1] * gg[2], g23 = gg[2] * gg[3];
+                const float x[8] = {kk[1] * gg[1] * kk[0], kk[2] * g12 * kk[0], kk[2] * gg[2] * kk[1],
+                                    kk[3] * (g12 * gg[3]) * kk[0], kk[3] * g23 * kk[1],
+                                    kk[3] * gg[3] * kk[2], 0.f, 0.f};
+                const float sum = warp_sum8(x, lane);
+                if ((lane & 3) == 0) sm.pairs[warp][lane >> 2] = sum;
             }
+            __syncthreads();
+            float4 y[kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float4 c = sm.kd[phase + 4 * i];
+                const float cj[kRows] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    y[j].x = fmaf(cj[j], s[i].x, y[j].x), y[j].y = fmaf(cj[j], s[i].y, y[j].y);
+                    y[j].z = fmaf(cj[j], s[i].z, y[j].z), y[j].w = fmaf(cj[j], s[i].w, y[j].w);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+#pragma unroll
+                for (int off = 8; off <= 16; off <<= 1) {
+                    y[j].x += __shfl_xor_sync(0xffffffffu, y[j].x, off);
+                    y[j].y += __shfl_xor_sync(0xffffffffu, y[j].y, off);
+                    y[j].z += __shfl_xor_sync(0xffffffffu, y[j].z, off);
+                    y[j].w += __shfl_xor_sync(0xffffffffu, y[j].w, off);
+                }
+            float pr[6];
+#pragma unroll
+            for (int e = 0; e < 6; ++e)
+                pr[e] = (sm.pairs[0][e] + sm.pairs[1][e]) + (sm.pairs[2][e] + sm.pairs[3][e]);
+            // u_j = beta_j (v_j - k_j d_j S - sum_{l<j} pair(j, l) u_l), in place of y
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                float4 r = make_float4(vv[j].x - y[j].x, vv[j].y - y[j].y, vv[j].z - y[j].z,
+                                       vv[j].w - y[j].w);
+#pragma unroll
+                for (int l = 0; l < j; ++l) {
+                    const float a = -pr[j * (j - 1) / 2 + l];
+                    r.x = fmaf(a, y[l].x, r.x), r.y = fmaf(a, y[l].y, r.y);
+                    r.z = fmaf(a, y[l].z, r.z), r.w = fmaf(a, y[l].w, r.w);
+                }
+                y[j] = make_float4(beta[j] * r.x, beta[j] * r.y, beta[j] * r.z, beta[j] * r.w);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float4 c = sm.ke[phase + 4 * i];
+                const float d = sm.end[phase + 4 * i];
+                s[i].x *= d, s[i].y *= d, s[i].z *= d, s[i].w *= d;
+                const float cj[kRows] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    s[i].x = fmaf(cj[j], y[j].x, s[i].x), s[i].y = fmaf(cj[j], y[j].y, s[i].y);
+                    s[i].z = fmaf(cj[j], y[j].z, s[i].z), s[i].w = fmaf(cj[j], y[j].w, s[i].w);
+                }
+            }
+            __syncthreads();   // the next rows' values take the place of these
         }
-        __syncthreads();   // the next group's rows take the place of these
+        float* out = p.S + (size_t)unit * kD * kD + phase * kD + col;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            __stcs(reinterpret_cast<float4*>(out + 4 * i * kD), s[i]);
+        unit = unit_next;
+        len = len_next;
     }
-
-    float* out = S + (size_t)(lane & 3) * kD + 16 * warp + 2 * (lane >> 2);
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        __stcs(reinterpret_cast<float2*>(out + (size_t)(4 * i) * kD), s[i]);
 }
 
-PerDevice g_tree_setup;
+PerDevice g_setup;
+int g_sms[PerDevice::kMax];   // written once per device, under g_setup
+
+template <typename Tin, int NB>
+cudaError_t set_tree() {
+    return cudaFuncSetAttribute(decode_tree_kernel<Tin, NB>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(TreeSmem<Tin, NB>));
+}
+
+cudaError_t set_up(int dev) {
+    cudaError_t e = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if ((e = set_tree<float, 1>()) != cudaSuccess || (e = set_tree<float, 2>()) != cudaSuccess ||
+        (e = set_tree<float, 4>()) != cudaSuccess ||
+        (e = set_tree<__nv_bfloat16, 1>()) != cudaSuccess ||
+        (e = set_tree<__nv_bfloat16, 2>()) != cudaSuccess ||
+        (e = set_tree<__nv_bfloat16, 4>()) != cudaSuccess)
+        return e;
+    if ((e = cudaFuncSetAttribute(commit_path_kernel<float>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)sizeof(PathSmem))) != cudaSuccess)
+        return e;
+    return cudaFuncSetAttribute(commit_path_kernel<__nv_bfloat16>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PathSmem));
+}
+
+template <typename Tin, int NB>
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
+    decode_tree_kernel<Tin, NB>
+        <<<(unsigned)(p.N * p.H), tree_threads(NB), sizeof(TreeSmem<Tin, NB>), stream>>>(p);
+    return cudaGetLastError();
+}
 
 template <typename Tin>
-cudaError_t launch_tree_typed(const TreeParams& p, cudaStream_t stream) {
-    const int bytes = TreeSmem((p.T + 15) & ~15).total * (int)sizeof(float);
-    decode_tree_kernel<Tin><<<(unsigned)(p.N * p.H), kThreads, bytes, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_tree_nodes(const TreeParams& p, cudaStream_t stream) {
+    if (p.T <= 16) return launch_tree<Tin, 1>(p, stream);
+    if (p.T <= 32) return launch_tree<Tin, 2>(p, stream);
+    return launch_tree<Tin, 4>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
-    const cudaError_t e = g_tree_setup.run([](int) {
-        const int most = TreeSmem(kMaxTreeNodes).total * (int)sizeof(float);
-        const cudaError_t a = cudaFuncSetAttribute(
-            decode_tree_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (a != cudaSuccess) return a;
-        return cudaFuncSetAttribute(decode_tree_kernel<__nv_bfloat16>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    });
+    const cudaError_t e = g_setup.run(set_up);
     if (e != cudaSuccess) return e;
-    return p.bf16 ? launch_tree_typed<__nv_bfloat16>(p, stream)
-                  : launch_tree_typed<float>(p, stream);
+    return p.bf16 ? launch_tree_nodes<__nv_bfloat16>(p, stream)
+                  : launch_tree_nodes<float>(p, stream);
 }
 
 cudaError_t launch_commit_path(const TreeParams& p, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)(p.N * p.H);
-    if (p.bf16) commit_path_kernel<__nv_bfloat16><<<blocks, kThreads, 0, stream>>>(p);
-    else commit_path_kernel<float><<<blocks, kThreads, 0, stream>>>(p);
+    int dev = 0;
+    const cudaError_t e = g_setup.run(set_up, &dev);
+    if (e != cudaSuccess) return e;
+    const int units = p.N * p.H;
+    const unsigned blocks = (unsigned)std::min(units, 2 * g_sms[dev]);
+    if (p.bf16)
+        commit_path_kernel<__nv_bfloat16>
+            <<<blocks, kPathThreads, sizeof(PathSmem), stream>>>(p, units);
+    else
+        commit_path_kernel<float><<<blocks, kPathThreads, sizeof(PathSmem), stream>>>(p, units);
     return cudaGetLastError();
 }
 
