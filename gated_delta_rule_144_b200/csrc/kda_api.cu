@@ -963,7 +963,8 @@ static kda_status_t check_tree_sizes(int N, int H, int T, kda_dtype_t dtype) {
         return fail(KDA_ERR_INVALID_ARG, "bad sizes N=%d H=%d T=%d", N, H, T);
     if (dtype != KDA_F32 && dtype != KDA_BF16)
         return fail(KDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
-    if ((int64_t)N * H > 0x7fffffffLL || (int64_t)N * T * H > (int64_t)1 << 40)
+    // (a TMA row coordinate counts 128 state rows per sequence and head)
+    if ((int64_t)N * H * 128 > 0x7fffffffLL || (int64_t)N * T * H > (int64_t)1 << 40)
         return fail(KDA_ERR_INVALID_ARG, "problem too large");
     return KDA_OK;
 }

@@ -12,9 +12,9 @@
 //
 // The tree: one block of 256 threads per (sequence, head), two per SM, up to 32 nodes (512 threads,
 // one per SM, above). Phases:
-//   load     S by bulk copies of its rows into shared memory, under way until the product; the
-//            rows of k and the gates.
-//   walk     a warp per node i walks i's ancestors, four at a time, with d_ij in registers (4
+//   load     S by TMA into shared memory, under way until the product; the rows of k and the
+//            gates.
+//   walk     a warp per node i walks i's ancestors with d_ij in registers (4
 //            channels per lane): only products of gates <= 1 appear, so no gate, -inf included,
 //            is out of range. It leaves the two scalars of each pair and the rows k_i d_i, q_i d_i.
 //   product  [k d; q d] S on the tensor cores (warp-level tf32 products: 16 x 8 x 8). The tree of
@@ -29,6 +29,7 @@
 #include <algorithm>
 
 #include "kda_sm100.cuh"
+#include "kda_tma.cuh"
 #include "kda_tree.cuh"
 
 namespace kda {
@@ -40,8 +41,7 @@ constexpr int kD = 128;
 // Threads of a tree's block: one per value column and block of nodes in the solve, 8 warps at least.
 constexpr int tree_threads(int nb) { return nb > 2 ? 512 : 256; }
 constexpr int kB = 16;       // nodes per block of the solve
-constexpr int kLd = 136;     // floats per state row in shared memory: a fragment's four rows start
-                             // 8 banks apart, so that half a warp's 8-byte loads do not collide
+constexpr int kLd = 136;     // floats per row of the products
 constexpr uint32_t kStateBytes = kD * kD * 4;
 constexpr uint32_t kWaitCycles = 1u << 31;   // about one second
 
@@ -61,6 +61,13 @@ __device__ __forceinline__ uint32_t tf32_rn(float x) {
     uint32_t r;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
+}
+
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Sum of x[i] over the warp's lanes; lane l returns the sum of x[l / 4].
@@ -132,8 +139,10 @@ __device__ __forceinline__ void mma_step(float (&c0)[4], float (&c1)[4], float4 
     mma_tf32_16x8x8(c0, ah, b0);
     mma_tf32_16x8x8(c1, ah, b1);
 }
-__device__ __forceinline__ const float* state_frag(const float* S, int ks, int cols, int lane) {
-    return S + (8 * ks + (lane & 3)) * kLd + cols + 2 * (lane >> 2);
+// Offset of state element (r, c) in shared memory: four 32-column panels as TMA lays them out with
+// the 128-byte swizzle (16-byte pieces permuted by row mod 8).
+__device__ __forceinline__ int state_at(int r, int c) {
+    return (c >> 5) * (kD * 32) + r * 32 + ((((c & 31) >> 2) ^ (r & 7)) << 2) + (c & 3);
 }
 // A tile's product to rows 0 .. 15 of x, columns cols .. cols + 15.
 __device__ __forceinline__ void store_tile(float* x, int cols, int lane, const float (&c0)[4],
@@ -143,19 +152,12 @@ __device__ __forceinline__ void store_tile(float* x, int cols, int lane, const f
     *reinterpret_cast<float4*>(p + 8 * kLd) = make_float4(c0[2], c1[2], c0[3], c1[3]);
 }
 
-// Warp 0: the state's rows into shared memory.
-__device__ __forceinline__ void fetch_state(float* s, const float* S, uint32_t bar, int lane) {
-    if (lane == 0) mbar_arrive_expect_tx(bar, kStateBytes);
-    __syncwarp();
-    for (int r = lane; r < kD; r += 32)
-        bulk_load(smem_u32(s + r * kLd), S + (size_t)r * kD, kD * 4, bar);
-}
-
 // NB: blocks of 16 nodes.
 template <typename Tin, int NB>
 struct TreeSmem {
     static constexpr int kN = kB * NB;
-    float state[kD * kLd];               // S, then the products: rows i of k d S, rows kN + i of q d S
+    // S, then the products: rows i of k d S, rows kN + i of q d S
+    float state[2 * kN * kLd > kD * kD ? 2 * kN * kLd : kD * kD];
     float rows[2 * kN * kD];             // k and the gates, then the left operand's fragments
     float akk[kN * kN], aqk[kN * kN];    // [j][i]: pairs of node i and j above it (and j = i)
     float u[NB > 1 ? kB * kD : 4];       // the block of u that the blocks behind take
@@ -169,10 +171,10 @@ struct TreeSmem {
 
 template <typename Tin, int NB>
 __global__ void __launch_bounds__(tree_threads(NB), NB <= 2 && sizeof(Tin) == 2 ? 2 : 1)
-decode_tree_kernel(const TreeParams p) {
+decode_tree_kernel(const __grid_constant__ CUtensorMap map, const TreeParams p) {
     using Smem = TreeSmem<Tin, NB>;
     constexpr int kN = Smem::kN, kThreads = tree_threads(NB), kWarps = kThreads / 32;
-    extern __shared__ __align__(16) uint8_t raw[];
+    extern __shared__ __align__(1024) uint8_t raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int unit = blockIdx.x, n = unit / p.H, h = unit % p.H, T = p.T;
@@ -183,14 +185,13 @@ decode_tree_kernel(const TreeParams p) {
     auto row = [&](int i) { return (((size_t)n * T + i) * p.H + h) * kD; };
     const uint32_t bar = smem_u32(&sm.bar);
 
-    if (warp == 0) {
-        if (lane == 0) {
-            mbar_init(bar, 1);
-            fence_mbar_init();
-            sm.bad_tree = 0;
-        }
-        __syncwarp();
-        fetch_state(sm.state, p.S + (size_t)unit * kD * kD, bar, lane);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(bar, kStateBytes);
+        for (int i = 0; i < 4; ++i)
+            tma_load_2d(smem_u32(sm.state + i * kD * 32), &map, bar, 32 * i, unit * kD);
+        sm.bad_tree = 0;
     }
     for (int i = tid; i < T * (kD / 4); i += kThreads) {
         const int r = i >> 5, c = 4 * (i & 31);
@@ -222,48 +223,63 @@ decode_tree_kernel(const TreeParams p) {
         return;
     }
 
-    // walk: nodes warp, warp + kWarps, ...; their rows stay in registers until every warp has read
-    // k and the gates
+    // walk: nodes warp, warp + kWarps, ..., two at a time (their chains interleave); their rows
+    // stay in registers until every warp has read k and the gates
     constexpr int kMine = kN / kWarps;
     float4 kd[kMine], qd[kMine];
 #pragma unroll
-    for (int b = 0; b < kMine; ++b) {
-        const int i = kWarps * b + warp;
-        kd[b] = qd[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-        unsigned long long above = 0;
-        if (sm.par[i] != -2) {
-            const float4 ki = load4(s_k + i * kD + 4 * lane), qi = load4(q + row(i) + 4 * lane);
-            float4 d = make_float4(1.f, 1.f, 1.f, 1.f);
-            int j = i;
-#pragma unroll 1
-            while (j >= 0) {
-                float x[8];
-                int at[4];
+    for (int b = 0; b < kMine; b += 2) {
+        float4 d[2];
+        int j[2];
+        unsigned long long above[2] = {0, 0};
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    at[m] = j;
-                    x[m] = x[4 + m] = 0.f;
-                    if (j >= 0) {
-                        const float4 kj = mul4(d, load4(s_k + j * kD + 4 * lane));
-                        x[m] = dot4(ki, kj);
-                        x[4 + m] = dot4(qi, kj);
-                        d = mul4(d, load4(s_g + j * kD + 4 * lane));
-                        above |= 1ull << j;
-                        j = sm.par[j];
+        for (int w = 0; w < 2; ++w) {
+            const int i = kWarps * (b + w) + warp;
+            j[w] = sm.par[i] != -2 ? i : -1;
+            d[w] = make_float4(1.f, 1.f, 1.f, 1.f);
+            kd[b + w] = qd[b + w] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j[w] >= 0) {
+                kd[b + w] = load4(s_k + i * kD + 4 * lane);
+                qd[b + w] = load4(q + row(i) + 4 * lane);
+            }
+        }
+#pragma unroll 1
+        while (j[0] >= 0 || j[1] >= 0) {
+            float x[8];
+            int at[4];   // pair (ancestor m, node w) at 2 m + w
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int e = 2 * m + w;
+                    at[e] = j[w];
+                    x[e] = x[4 + e] = 0.f;
+                    if (j[w] >= 0) {
+                        const float4 kj = mul4(d[w], load4(s_k + j[w] * kD + 4 * lane));
+                        x[e] = dot4(kd[b + w], kj);
+                        x[4 + e] = dot4(qd[b + w], kj);
+                        d[w] = mul4(d[w], load4(s_g + j[w] * kD + 4 * lane));
+                        above[w] |= 1ull << j[w];
+                        j[w] = sm.par[j[w]];
                     }
                 }
-                const float sum = warp_sum8(x, lane);
-                const int m = lane >> 2 & 3;
-                const int to = m == 0 ? at[0] : m == 1 ? at[1] : m == 2 ? at[2] : at[3];
-                if ((lane & 3) == 0 && to >= 0) {
-                    if (lane < 16) sm.akk[to * kN + i] = to == i ? 0.f : sum;
-                    else sm.aqk[to * kN + i] = sum;
-                }
+            const float sum = warp_sum8(x, lane);
+            const int e = lane >> 2 & 3, i = kWarps * (b + (e & 1)) + warp;
+            const int to = e == 0 ? at[0] : e == 1 ? at[1] : e == 2 ? at[2] : at[3];
+            if ((lane & 3) == 0 && to >= 0) {
+                if (lane < 16) sm.akk[to * kN + i] = to == i ? 0.f : sum;
+                else sm.aqk[to * kN + i] = sum;
             }
-            kd[b] = mul4(ki, d);
-            qd[b] = mul4(qi, d);
         }
-        if (lane == 0) sm.above[i] = above & ~(1ull << i);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int i = kWarps * (b + w) + warp;
+            if (sm.par[i] != -2) {
+                kd[b + w] = mul4(kd[b + w], d[w]);
+                qd[b + w] = mul4(qd[b + w], d[w]);
+            }
+            if (lane == 0) sm.above[i] = above[w] & ~(1ull << i);
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -275,13 +291,8 @@ decode_tree_kernel(const TreeParams p) {
     const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and block of nodes
     float y[kB], r[kB];
     if (blk < NB) {
-        const Tin* at = v + row(kB * blk) + col;
-        const size_t step = (size_t)p.H * kD;
 #pragma unroll
-        for (int i = 0; i < kB; ++i) {
-            r[i] = 0.f;
-            if (sm.par[kB * blk + i] != -2) r[i] = load_elem(at, i * step);
-        }
+        for (int i = 0; i < kB; ++i) r[i] = load_elem(v, row(min(kB * blk + i, T - 1)) + col);
     }
     const bool ok = mbar_wait(bar, 0, kWaitCycles);
     if (!ok) set_device_error(p.err, DEV_TIMEOUT);
@@ -291,6 +302,8 @@ decode_tree_kernel(const TreeParams p) {
         constexpr int kTiles = 2 * NB / (kWarps / 8);
         const int cols = 16 * (warp & 7), t0 = (warp >> 3) * kTiles;
         const float* frag = sm.rows + t0 * 2048;
+        const int at0 = state_at(lane & 3, cols + 2 * (lane >> 2));
+        const int at1 = state_at((lane & 3) + 4, cols + 2 * (lane >> 2));
         float c0[kTiles][4], c1[kTiles][4];
 #pragma unroll
         for (int b = 0; b < kTiles; ++b)
@@ -298,9 +311,8 @@ decode_tree_kernel(const TreeParams p) {
             for (int e = 0; e < 4; ++e) c0[b][e] = c1[b][e] = 0.f;
 #pragma unroll 4
         for (int ks = 0; ks < 16; ++ks) {
-            const float* at = state_frag(sm.state, ks, cols, lane);
-            const float2 s0 = *reinterpret_cast<const float2*>(at);
-            const float2 s1 = *reinterpret_cast<const float2*>(at + 4 * kLd);
+            const float2 s0 = *reinterpret_cast<const float2*>(sm.state + at0 + ks * 256);
+            const float2 s1 = *reinterpret_cast<const float2*>(sm.state + at1 + ks * 256);
 #pragma unroll
             for (int b = 0; b < kTiles; ++b)
                 mma_step<sizeof(Tin) == 4>(c0[b], c1[b], load_frag(frag + b * 2048, ks, lane), s0, s1);
@@ -320,7 +332,7 @@ decode_tree_kernel(const TreeParams p) {
     if (blk < NB) {
 #pragma unroll
         for (int i = 0; i < kB; ++i) {
-            r[i] -= sm.state[(kB * blk + i) * kLd + col];
+            r[i] = sm.par[kB * blk + i] != -2 ? r[i] - sm.state[(kB * blk + i) * kLd + col] : 0.f;
             y[i] = sm.state[(kN + kB * blk + i) * kLd + col];
         }
     }
@@ -352,8 +364,10 @@ decode_tree_kernel(const TreeParams p) {
                         }
                 }
                 if (NB > 1) sm.u[j * kD + col] = u;
-                if (sm.par[at] != -2) store_elem(o, row(at) + col, y[j]);
             }
+#pragma unroll
+            for (int j = 0; j < kB; ++j)
+                if (sm.par[kB * b + j] != -2) store_elem(o, row(kB * b + j) + col, y[j]);
             if (NB > 1) sm.bad[col] = bad;
         }
         if (NB > 1 && b + 1 < NB) {
@@ -381,113 +395,146 @@ decode_tree_kernel(const TreeParams p) {
     }
 }
 
-// The commit. One 128-thread block per SM half walks the (sequence, head) units: while it works on
-// one unit's state in registers, the next one's streams into shared memory. Rows are taken four at
-// a time: thread c holds channel c of the rows (their products of gates are its own running
-// products), then, as (row phase, four columns), 32 rows of the state: k d S, the substitution for
-// u in registers, and S = d_e S + sum_j (d_ej k_j) u_j^T, each one pass over the registers of 4 rows'
-// multiply-adds. (Tensor-core products of 16-row tiles, split for fp32, cost more instructions up
-// to about 9 rows: 567 us against 368 us with the state in registers and 512 threads per unit.)
+// The commit. Two blocks per SM walk the (sequence, head) units: four warps work on one unit's state
+// in registers while a fifth brings the next unit's state and first rows into shared memory by bulk
+// copies. Rows are taken four at a time: thread c holds channel c of the rows (their products of
+// gates are its own running products), then, as (row phase, four columns), 32 rows of the state:
+// k d S, the substitution for u in registers, and S = d_e S + sum_j (d_ej k_j) u_j^T, each one pass
+// over the registers. (Tensor-core products of 16-row tiles, split for fp32, take more instructions
+// up to about 9 rows.)
 constexpr int kRows = 4;
-constexpr int kPathThreads = 128;
+constexpr int kPathWorkers = 128, kPathThreads = kPathWorkers + 32;
+template <typename Tin>
 struct PathSmem {
     float state[kD * kD];           // the next unit's state
+    Tin k[2][kRows][kD], v[2][kRows][kD];   // first rows of this unit and the next
+    float g[2][kRows][kD];
     float4 kd[kD], ke[kD];          // [channel][row]: k_j d_j, d_ej k_j
     float end[kD];                  // d_e
     float pairs[4][8];              // per warp: pair sums
-    unsigned long long bar;
+    int unit[2], len[2];            // (unit at the end of the walk: -1)
+    unsigned long long full[2], free;
 };
 
 template <typename Tin>
 __global__ void __launch_bounds__(kPathThreads, 2)
 commit_path_kernel(const TreeParams p, const int units) {
     extern __shared__ __align__(16) uint8_t raw[];
-    PathSmem& sm = *reinterpret_cast<PathSmem*>(raw);
+    PathSmem<Tin>& sm = *reinterpret_cast<PathSmem<Tin>*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int phase = lane >> 3, col = 32 * warp + 4 * (lane & 7);
     const Tin* k = static_cast<const Tin*>(p.k);
     const Tin* v = static_cast<const Tin*>(p.v);
-    const uint32_t bar = smem_u32(&sm.bar);
-
-    // length of a unit's path: up to its first negative entry; -1 where it leaves the rows
-    auto length = [&](int unit) {
-        const int32_t* path = p.nodes + (size_t)(unit / p.H) * p.A;
-        int len = p.A;
-        bool bad = false;
-        for (int i = lane; i - lane < len; i += 32) {   // every warp for itself
-            const int r = i < p.A ? path[i] : -1;
-            const unsigned stop = __ballot_sync(0xffffffffu, r < 0);
-            const int here = stop ? __ffs(stop) - 1 : 32;
-            bad |= lane < here && r >= p.T;
-            if (stop) len = i - lane + here;
-        }
-        return __any_sync(0xffffffffu, bad) ? -1 : len;
-    };
-    // the next unit at or behind u with rows to commit, its length
-    auto next = [&](int u, int* len) {
-        for (; u < units; u += gridDim.x) {
-            *len = length(u);
-            if (*len > 0) break;
-            if (*len < 0 && tid == 0) set_device_error(p.err, DEV_BAD_INDEX);
-        }
-        return u;
-    };
-    auto fetch = [&](int u) {
-        if (tid == 0) {
-            mbar_arrive_expect_tx(bar, kStateBytes);
-            for (int i = 0; i < 4; ++i)
-                bulk_load(smem_u32(sm.state) + i * (kStateBytes / 4),
-                          p.S + (size_t)u * kD * kD + i * (kD * kD / 4), kStateBytes / 4, bar);
-        }
-    };
+    const uint32_t full = smem_u32(sm.full), free = smem_u32(&sm.free);
     if (tid == 0) {
-        mbar_init(bar, 1);
+        mbar_init(full, 1);
+        mbar_init(full + 8, 1);
+        mbar_init(free, kPathWorkers);
         fence_mbar_init();
     }
     __syncthreads();
-    int len = 0, unit = next(blockIdx.x, &len);
-    if (unit < units) fetch(unit);
 
-    for (int it = 0; unit < units; ++it) {
+    if (warp == kPathWorkers / 32) {   // ------------------------------------------------ loader
+        int it = 0;
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
+            // the path's length: up to its first negative entry; nothing is done where it leaves
+            // the rows
+            const int n = unit / p.H, h = unit % p.H;
+            const int32_t* path = p.nodes + (size_t)n * p.A;
+            int len = p.A, first = -1;
+            bool bad = false;
+            for (int i0 = 0; i0 < len; i0 += 32) {
+                const int r = i0 + lane < p.A ? path[i0 + lane] : -1;
+                const unsigned stop = __ballot_sync(0xffffffffu, r < 0);
+                const int here = stop ? __ffs(stop) - 1 : 32;
+                bad |= lane < here && r >= p.T;
+                if (i0 == 0) first = r;
+                if (stop) len = i0 + here;
+            }
+            if (__any_sync(0xffffffffu, bad)) {
+                if (lane == 0) set_device_error(p.err, DEV_BAD_INDEX);
+                continue;
+            }
+            if (len == 0) continue;
+            // the workers have the previous state in registers, and are done with this buffer's
+            // rows
+            if (it > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(free, (it - 1) & 1, kWaitCycles));
+                if (!ok) break;
+            }
+            const int b = it & 1, m = min(len, kRows);
+            const uint32_t bar = full + 8 * b;
+            if (lane == 0) {
+                sm.unit[b] = unit;
+                sm.len[b] = len;
+                mbar_arrive_expect_tx(bar, kStateBytes + m * kD * (2 * sizeof(Tin) + 4));
+                for (int i = 0; i < 4; ++i)
+                    bulk_load(smem_u32(sm.state) + i * (kStateBytes / 4),
+                              p.S + (size_t)unit * kD * kD + i * (kD * kD / 4), kStateBytes / 4,
+                              bar);
+            }
+            __syncwarp();
+            if (lane < m) {
+                const size_t at = (((size_t)n * p.T + first) * p.H + h) * kD;
+                bulk_load(smem_u32(sm.k[b][lane]), k + at, kD * sizeof(Tin), bar);
+                bulk_load(smem_u32(sm.v[b][lane]), v + at, kD * sizeof(Tin), bar);
+                bulk_load(smem_u32(sm.g[b][lane]), p.log_g + at, kD * 4, bar);
+            }
+            __syncwarp();
+            ++it;
+        }
+        if (!ok) {   // the copy in flight lands first
+            if (lane == 0) set_device_error(p.err, DEV_TIMEOUT);
+            mbar_wait(full + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1, kWaitCycles);
+            return;
+        }
+        if (it > 0) ok = __all_sync(0xffffffffu, mbar_wait(free, (it - 1) & 1, kWaitCycles));
+        if (lane == 0) {
+            sm.unit[it & 1] = -1;
+            mbar_arrive_expect_tx(full + 8 * (it & 1), 0);
+        }
+        return;
+    }
+
+    // ------------------------------------------------------------------------------ workers
+    const int phase = lane >> 3, col = 32 * warp + 4 * (lane & 7);
+    for (int it = 0;; ++it) {
+        const int b = it & 1;
+        const bool ok = mbar_wait(full + 8 * b, (it >> 1) & 1, kWaitCycles);
+        if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) set_device_error(p.err, DEV_TIMEOUT);
+            return;
+        }
+        const int unit = sm.unit[b], len = sm.len[b];
+        if (unit < 0) return;
         const int n = unit / p.H, h = unit % p.H;
         const int32_t* path = p.nodes + (size_t)n * p.A;
         auto row = [&](int a) { return (((size_t)n * p.T + path[a]) * p.H + h) * kD; };
-        // the first rows' values, while the state lands
-        float kk[kRows], gg[kRows];
-        auto rows = [&](int a0) {
+        float beta[kRows];   // of the first rows
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            beta[j] = j < len ? load_elem(static_cast<const Tin*>(p.beta),
+                                          ((int64_t)n * p.T + path[j]) * p.H + h)
+                              : 0.f;
+        float4 s[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = load4(sm.state + (phase + 4 * i) * kD + col);
+        mbar_arrive(free);
+
+        for (int a0 = 0; a0 < len; a0 += kRows) {
+            float kk[kRows], gg[kRows];
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
                 kk[j] = 0.f;
                 gg[j] = 1.f;
-                if (a0 + j < len) {
+                if (a0 + j >= len) continue;
+                if (a0 == 0) {
+                    kk[j] = load_elem(sm.k[b][j], tid);
+                    gg[j] = expf(sm.g[b][j][tid]);
+                } else {
                     const size_t at = row(a0 + j) + tid;
                     kk[j] = load_elem(k, at);
                     gg[j] = expf(p.log_g[at]);
-                }
-            }
-        };
-        rows(0);
-        const bool ok = mbar_wait(bar, it & 1, kWaitCycles);
-        if (!ok) set_device_error(p.err, DEV_TIMEOUT);
-        if (__syncthreads_or(!ok)) return;
-        float4 s[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = load4(sm.state + (phase + 4 * i) * kD + col);
-        __syncthreads();
-        int len_next = 0;
-        const int unit_next = next(unit + gridDim.x, &len_next);
-        if (unit_next < units) fetch(unit_next);
-
-        for (int a0 = 0; a0 < len; a0 += kRows) {
-            if (a0 > 0) rows(a0);
-            float4 vv[kRows];
-            float beta[kRows];
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                vv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                beta[j] = 0.f;
-                if (a0 + j < len) {
-                    vv[j] = load4(v + row(a0 + j) + col);
                     beta[j] = load_elem(static_cast<const Tin*>(p.beta),
                                         ((int64_t)n * p.T + path[a0 + j]) * p.H + h);
                 }
@@ -495,6 +542,7 @@ commit_path_kernel(const TreeParams p, const int units) {
             // channel tid: products of gates up to each row, from behind each row, between rows
             const float p0 = gg[0], p1 = p0 * gg[1], p2 = p1 * gg[2], p3 = p2 * gg[3];
             const float q2 = gg[3], q1 = gg[2] * q2, q0 = gg[1] * q1;
+            bar_sync(1, kPathWorkers);   // everyone has read the rows before these
             sm.kd[tid] = make_float4(kk[0] * p0, kk[1] * p1, kk[2] * p2, kk[3] * p3);
             sm.ke[tid] = make_float4(kk[0] * q0, kk[1] * q1, kk[2] * q2, kk[3]);
             sm.end[tid] = p3;
@@ -506,7 +554,7 @@ commit_path_kernel(const TreeParams p, const int units) {
                 const float sum = warp_sum8(x, lane);
                 if ((lane & 3) == 0) sm.pairs[warp][lane >> 2] = sum;
             }
-            __syncthreads();
+            bar_sync(1, kPathWorkers);
             float4 y[kRows];
 #pragma unroll
             for (int j = 0; j < kRows; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -529,22 +577,22 @@ commit_path_kernel(const TreeParams p, const int units) {
                     y[j].z += __shfl_xor_sync(0xffffffffu, y[j].z, off);
                     y[j].w += __shfl_xor_sync(0xffffffffu, y[j].w, off);
                 }
-            float pr[6];
-#pragma unroll
-            for (int e = 0; e < 6; ++e)
-                pr[e] = (sm.pairs[0][e] + sm.pairs[1][e]) + (sm.pairs[2][e] + sm.pairs[3][e]);
             // u_j = beta_j (v_j - k_j d_j S - sum_{l<j} pair(j, l) u_l), in place of y
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
-                float4 r = make_float4(vv[j].x - y[j].x, vv[j].y - y[j].y, vv[j].z - y[j].z,
-                                       vv[j].w - y[j].w);
+                float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (a0 + j < len) r = a0 == 0 ? load4(sm.v[b][j] + col) : load4(v + row(a0 + j) + col);
+                r = make_float4(r.x - y[j].x, r.y - y[j].y, r.z - y[j].z, r.w - y[j].w);
 #pragma unroll
                 for (int l = 0; l < j; ++l) {
-                    const float a = -pr[j * (j - 1) / 2 + l];
+                    const int e = j * (j - 1) / 2 + l;
+                    const float a = -((sm.pairs[0][e] + sm.pairs[1][e]) +
+                                      (sm.pairs[2][e] + sm.pairs[3][e]));
                     r.x = fmaf(a, y[l].x, r.x), r.y = fmaf(a, y[l].y, r.y);
                     r.z = fmaf(a, y[l].z, r.z), r.w = fmaf(a, y[l].w, r.w);
                 }
                 y[j] = make_float4(beta[j] * r.x, beta[j] * r.y, beta[j] * r.z, beta[j] * r.w);
+                beta[j] = 0.f;   // (rows behind the path's end)
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -558,14 +606,11 @@ commit_path_kernel(const TreeParams p, const int units) {
                     s[i].z = fmaf(cj[j], y[j].z, s[i].z), s[i].w = fmaf(cj[j], y[j].w, s[i].w);
                 }
             }
-            __syncthreads();   // the next rows' values take the place of these
         }
         float* out = p.S + (size_t)unit * kD * kD + phase * kD + col;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             __stcs(reinterpret_cast<float4*>(out + 4 * i * kD), s[i]);
-        unit = unit_next;
-        len = len_next;
     }
 }
 
@@ -590,16 +635,22 @@ cudaError_t set_up(int dev) {
         return e;
     if ((e = cudaFuncSetAttribute(commit_path_kernel<float>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)sizeof(PathSmem))) != cudaSuccess)
+                                  (int)sizeof(PathSmem<float>))) != cudaSuccess)
         return e;
     return cudaFuncSetAttribute(commit_path_kernel<__nv_bfloat16>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PathSmem));
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(PathSmem<__nv_bfloat16>));
 }
 
 template <typename Tin, int NB>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
+    CUtensorMap map;
+    const cudaError_t e = make_map_2d(&map, p.S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                                      (unsigned long long)p.N * p.H * kD, kD, 32, kD,
+                                      CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
     decode_tree_kernel<Tin, NB>
-        <<<(unsigned)(p.N * p.H), tree_threads(NB), sizeof(TreeSmem<Tin, NB>), stream>>>(p);
+        <<<(unsigned)(p.N * p.H), tree_threads(NB), sizeof(TreeSmem<Tin, NB>), stream>>>(map, p);
     return cudaGetLastError();
 }
 
@@ -627,9 +678,10 @@ cudaError_t launch_commit_path(const TreeParams& p, cudaStream_t stream) {
     const unsigned blocks = (unsigned)std::min(units, 2 * g_sms[dev]);
     if (p.bf16)
         commit_path_kernel<__nv_bfloat16>
-            <<<blocks, kPathThreads, sizeof(PathSmem), stream>>>(p, units);
+            <<<blocks, kPathThreads, sizeof(PathSmem<__nv_bfloat16>), stream>>>(p, units);
     else
-        commit_path_kernel<float><<<blocks, kPathThreads, sizeof(PathSmem), stream>>>(p, units);
+        commit_path_kernel<float>
+            <<<blocks, kPathThreads, sizeof(PathSmem<float>), stream>>>(p, units);
     return cudaGetLastError();
 }
 
