@@ -806,29 +806,33 @@ static int linear_walk_segment(const kda_linear_desc_t* d) {
 
 // Tokens per segment of the chunked kernel (0: whole sequences), whose CTAs take one (segment,
 // head, 64 value columns) each, one per SM. Equal lengths: the count of segments with the least
-// modelled time, in units of one chunk: waves of m chunks with outputs, and before them the
-// states of all segments but the last at half a chunk each, plus 2 units per CTA and 4 for the two
-// further launches. Packed documents, whose lengths the host does not see: segments of an SM's
-// even share of all chunks, at least 8.
+// modelled time, in units of one chunk with outputs (about 2 us): waves of m such chunks, and
+// before them the states of all segments but the last at 0.65 of a chunk each, 3 units per CTA's
+// start and end, 1 for the further launch. Packed documents, whose lengths the host does not see,
+// are cut only where one takes much more than an SM's even share of all chunks (the CTAs take the
+// longest first, so shorter ones pack well).
 static int linear_chunk_segment(const kda_linear_desc_t* d, bool packed) {
     const int n = (d->T + kda::kLinearChunk - 1) / kda::kLinearChunk;
     const double units = (double)d->H * ((d->dv + 63) / 64), sms = 148.0;
-    if (packed) {
-        const int m = std::max(8, (int)std::ceil(n * units / sms));
+    if (packed && d->num_seqs > 1) {
+        const int m = std::max(8, (int)std::ceil(1.25 * n * units / sms));
         return n > m ? m * kda::kLinearChunk : 0;
     }
     const double all = units * d->num_seqs;
-    double best = std::ceil(all / sms) * (n + 2.0);
+    double best = std::ceil(all / sms) * (n + 3.0);
     int m_best = 0;
     for (int m = 1; m < n; ++m) {
         const int P = (n + m - 1) / m;
         if (P > 64) continue;
-        const double cost = std::ceil(all * (P - 1) / sms) * (0.5 * m + 2.0) +
-                            std::ceil(all * P / sms) * (m + 2.0) + 4.0;
+        const double cost = std::ceil(all * (P - 1) / sms) * (0.65 * m + 3.0) +
+                            std::ceil(all * P / sms) * (m + 3.0) + 1.0;
         if (cost < best) best = cost, m_best = m;
     }
     return m_best * kda::kLinearChunk;
 }
+
+// Segments up to which the chunked kernel's CTAs chain their own initial state.
+constexpr int kChainedSegments = 12;
 
 static int linear_segment(const kda_linear_desc_t* d, bool packed) {
     if (d->num_seqs > 1024 || d->H > 65535) return 0;   // enough sequences to fill the GPU
@@ -912,10 +916,13 @@ kda_status_t kda_linear_fwd(const kda_linear_desc_t* d, const void* q, const voi
     p.slots = L.slots;
     p.seg_state = static_cast<float*>(workspace);
     p.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.decay);
-    if (cu_seqlens && (e = kda::launch_linear_check(p, s)) != cudaSuccess)
+    const bool chunked = linear_chunked(d);
+    if (cu_seqlens && !chunked && (e = kda::launch_linear_check(p, s)) != cudaSuccess)
         return cuda_fail(e, "kda_linear_fwd cu_seqlens check");
-    if ((e = pass(kda::LinearPass::kStates)) != cudaSuccess ||
-        (e = kda::launch_linear_combine(p, s)) != cudaSuccess ||
+    if ((e = pass(kda::LinearPass::kStates)) != cudaSuccess)
+        return cuda_fail(e, "kda_linear_fwd launch");
+    p.seg_ready = !chunked || d->T > kChainedSegments * L.seg_tokens;
+    if ((p.seg_ready && (e = kda::launch_linear_combine(p, s)) != cudaSuccess) ||
         (e = pass(kda::LinearPass::kOutputs)) != cudaSuccess)
         return cuda_fail(e, "kda_linear_fwd launch");
     return KDA_OK;

@@ -136,10 +136,11 @@ linear_walk_kernel(const LinearParams p, const LinearPass pass, const int col_gr
 }
 
 // The state before segment s of a sequence is d_{s-1} (state before s - 1) + B_{s-1}; the B of a
-// slot gives way to its initial state. One thread per state element; the loads of the next B and
-// decay do not wait for the chain.
+// slot gives way to its initial state. One thread per state element; the loads of kAhead segments
+// do not wait for the chain.
 __global__ void __launch_bounds__(256)
 linear_combine_kernel(const LinearParams p) {
+    constexpr int kAhead = 8;
     const int unit = p.dk * p.dv;
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int n = blockIdx.z, h = blockIdx.y;
@@ -159,17 +160,22 @@ linear_combine_kernel(const LinearParams p) {
     float* st = p.seg_state + ((size_t)first * p.H + h) * unit + e;
     const float* dc = p.seg_decay + (size_t)first * p.H + h;
     const size_t step = (size_t)p.H * unit;
-    float b = st[0], d = dc[0];
-    for (int s = 0; s + 1 < segs; ++s) {
-        float bn = 0.f, dn = 0.f;
-        if (s + 2 < segs) {
-            bn = st[(size_t)(s + 1) * step];
-            dn = dc[(size_t)(s + 1) * p.H];
-        }
-        S = fmaf(d, S, b);
-        st[(size_t)(s + 1) * step] = S;
-        b = bn;
-        d = dn;
+    float carry = st[0];
+    for (int s0 = 0; s0 + 1 < segs; s0 += kAhead) {   // reads B of s0 .. s0 + kAhead first
+        float b[kAhead], d[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s0 + i + 1 < segs) {
+                b[i] = i == 0 ? carry : st[(size_t)(s0 + i) * step];
+                d[i] = dc[(size_t)(s0 + i) * p.H];
+            }
+        if (s0 + kAhead + 1 < segs) carry = st[(size_t)(s0 + kAhead) * step];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s0 + i + 1 < segs) {
+                S = fmaf(d[i], S, b[i]);
+                st[(size_t)(s0 + i + 1) * step] = S;
+            }
     }
 }
 

@@ -31,6 +31,7 @@ struct LinearParams {
     int slots;                  // slots per head (N without segments)
     float* seg_state;           // [slots, H, dk, dv]: B, then the segment's initial state
     float* seg_decay;           // [slots, H]
+    bool seg_ready;             // chunked outputs: seg_state has been chained by launch_linear_combine
 };
 
 enum class LinearPass {

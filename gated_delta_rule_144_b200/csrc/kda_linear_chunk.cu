@@ -148,6 +148,89 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// What a CTA works on: segment `seg` of sequence n (rows [begin, end)), its place among the slots.
+struct ChunkSlot {
+    int n, seg, slot;
+    long long begin, end;
+    bool last;
+};
+constexpr int kSorted = 1024;   // packed slots up to which CTAs take them longest first
+
+// The CTA's g-th slot, found by the whole block; `tmp` is kSorted ints of shared memory. Equal
+// lengths: first segments first (they wait for nothing). Packed: longest first up to kSorted
+// slots, so that no long one starts last; every CTA reads all offsets, and a malformed cu_seqlens
+// makes each of them report it and stop. False: nothing to do.
+__device__ __forceinline__ bool chunk_slot(const LinearParams& p, int g, int tid, int* tmp,
+                                           ChunkSlot* s) {
+    const int L = p.seg_tokens;
+    if (!p.cu_seqlens) {
+        const int segs = L > 0 ? max(1, (p.T + L - 1) / L) : 1;
+        s->seg = g / p.N;
+        s->n = g % p.N;
+        s->slot = s->n * segs + s->seg;
+        const long long t0 = (long long)s->n * p.T;
+        s->begin = t0 + (long long)s->seg * L;
+        s->end = L > 0 ? min(t0 + p.T, s->begin + L) : t0 + p.T;
+        s->last = s->seg == segs - 1;
+        return true;
+    }
+    const int32_t* __restrict__ cu = p.cu_seqlens;
+    bool bad = false;
+    for (int i = tid; i <= p.N; i += kThreads) {
+        const int c = cu[i];
+        bad |= (i == 0 && c != 0) || (i == p.N && c != p.T) || (i < p.N && cu[i + 1] < c);
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) set_device_error(p.err, DEV_BAD_SEQLENS);
+        return false;
+    }
+    // slot of (n, segment 0): floor(cu[n] / L) + n, or n; rows of slot i of sequence n
+    auto first = [&](int n) { return L > 0 ? cu[n] / L + n : n; };
+    auto rows = [&](int n, int slot) {
+        const int len = cu[n + 1] - cu[n], at = L > 0 ? (slot - first(n)) * L : 0;
+        return at == 0 ? (L > 0 ? min(len, L) : len) : at < len ? min(len - at, L) : -1;
+    };
+    int slot = g;
+    if (p.slots <= kSorted) {
+        for (int i = tid; i < p.slots; i += kThreads) tmp[i] = -1;   // (slots that nothing uses)
+        __syncthreads();
+        for (int n = tid; n < p.N; n += kThreads)
+            for (int i = first(n); i < p.slots; ++i) {
+                const int r = rows(n, i);
+                if (r < 0) break;
+                tmp[i] = r;
+                if (L <= 0) break;
+            }
+        __syncthreads();
+        int mine = -1;   // the slot with g slots before it
+        for (int i = tid; i < p.slots; i += kThreads) {
+            const int r = tmp[i];
+            int before = 0;
+            for (int j = 0; j < p.slots; ++j) {
+                const int x = tmp[j];
+                before += x > r || (x == r && j < i);
+            }
+            if (before == g) mine = i;
+        }
+        __syncthreads();
+        if (mine >= 0) tmp[0] = mine;
+        __syncthreads();
+        slot = tmp[0];
+    }
+    int below = 0;   // sequences whose first slot is not behind this one
+    for (int i0 = 0; i0 < p.N; i0 += kThreads)
+        below += __syncthreads_count(i0 + tid < p.N && first(i0 + tid) <= slot);
+    const int n = below - 1, r = rows(n, slot);
+    if (r < 0) return false;
+    s->n = n;
+    s->slot = slot;
+    s->seg = slot - first(n);
+    s->begin = cu[n] + (long long)s->seg * L;
+    s->end = s->begin + r;
+    s->last = s->end == cu[n + 1];
+    return true;
+}
+
 // kOut: outputs (kWhole, kOutputs); else the states of segments (kStates).
 template <bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -159,8 +242,10 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     const int tile = blockIdx.x % args.tiles;
     const int h = blockIdx.x / args.tiles % p.H, g = blockIdx.x / args.tiles / p.H;
     const int hk = h / (p.H / p.Hk);
-    LinearSlot sl;
-    if (!linear_slot(p, g, &sl)) return;
+    ChunkSlot sl;
+    if (!chunk_slot(p, g, tid, reinterpret_cast<int*>(sm), &sl)) return;
+    // the outputs' launch may start now; what it reads of this one it waits for
+    if (!kOut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!kOut && sl.last) return;
     const int nchunks = (int)((sl.end - sl.begin + kC - 1) / kC);
     const int j0 = tile * kNV;
@@ -342,17 +427,34 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         // ============================================================ state
         const size_t unit = (size_t)p.dk * p.dv;
         const size_t at = (size_t)row * p.dv + j0;
-        const float* init = nullptr;
-        if (kOut)
-            init = sl.seg > 0 ? p.seg_state + ((size_t)g * p.H + h) * unit
-                              : (p.h0 ? p.h0 + ((size_t)sl.n * p.H + h) * unit : nullptr);
         float S[kNV];
 #pragma unroll
-        for (int i = 0; i < kNV; i += 4) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (init && row < p.dk && j0 + i < p.dv)
-                x = *reinterpret_cast<const float4*>(init + at + i);
-            S[i] = x.x, S[i + 1] = x.y, S[i + 2] = x.z, S[i + 3] = x.w;
+        for (int i = 0; i < kNV; ++i) S[i] = 0.f;
+        // S <- f S + what is at `from`
+        auto add = [&](const float* from, float f) {
+            if (row >= p.dk) return;
+#pragma unroll
+            for (int i = 0; i < kNV; i += 4) {
+                if (j0 + i >= p.dv) continue;
+                const float4 x = *reinterpret_cast<const float4*>(from + at + i);
+                S[i] = fmaf(f, S[i], x.x), S[i + 1] = fmaf(f, S[i + 1], x.y);
+                S[i + 2] = fmaf(f, S[i + 2], x.z), S[i + 3] = fmaf(f, S[i + 3], x.w);
+            }
+        };
+        if (kOut) {
+            // h0; for a later segment the states of those before it on top of it, or, where they
+            // are many, their sum from a launch of its own (seg_ready)
+            const bool ready = p.seg_ready && sl.seg > 0;
+            if (sl.seg > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll 1
+            for (int i = ready ? 0 : sl.seg; i >= 0; --i) {
+                const size_t from = (size_t)(sl.slot - i) * p.H + h;
+                const bool start = i == sl.seg && !ready;
+                if (start && !p.h0) continue;
+                add(start ? p.h0 + ((size_t)sl.n * p.H + h) * unit
+                          : p.seg_state + (ready ? from : from - p.H) * unit,
+                    start || ready ? 0.f : p.seg_decay[from - p.H]);
+            }
         }
         auto publish = [&] {   // bf16 S, row `row`
             uint8_t* to = sm + OFF_SB + row * 128;
@@ -396,7 +498,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             }
         }
         float* out = kOut ? (sl.last && p.hT ? p.hT + ((size_t)sl.n * p.H + h) * unit : nullptr)
-                          : p.seg_state + ((size_t)g * p.H + h) * unit;
+                          : p.seg_state + ((size_t)sl.slot * p.H + h) * unit;
         if (out && !failed && row < p.dk) {
 #pragma unroll
             for (int i = 0; i < kNV; i += 4)
@@ -404,7 +506,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                     *reinterpret_cast<float4*>(out + at + i) =
                         make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
         }
-        if (!kOut && tile == 0 && row == 0) p.seg_decay[(size_t)g * p.H + h] = exp2f(decay);
+        if (!kOut && tile == 0 && row == 0) p.seg_decay[(size_t)sl.slot * p.H + h] = exp2f(decay);
     } else if (warp < 12) {
         // ============================================================ values
         // 32 rows at a time: lane r takes row r of a quarter, the warp 16 of the columns
@@ -658,6 +760,8 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         }
     }
     if (failed && lane == 0) set_device_error(p.err, DEV_TIMEOUT);
+    // (this launch does not end before the one that it may have overtaken)
+    if (kOut && warp == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tbase, kTmemCols);
@@ -712,11 +816,22 @@ cudaError_t launch_linear_chunk(const LinearParams& p, LinearPass pass, cudaStre
         (e = map(&m.v, p.v, p.H, p.dv)) != cudaSuccess ||
         (e = map(&m.o, p.o, p.H, p.dv)) != cudaSuccess)
         return e;
-    if (pass == LinearPass::kStates)
+    if (pass == LinearPass::kStates) {
         linear_chunk_kernel<false><<<(unsigned)blocks, kThreads, kSmem, stream>>>(m, a);
-    else
-        linear_chunk_kernel<true><<<(unsigned)blocks, kThreads, kSmem, stream>>>(m, a);
-    return cudaGetLastError();
+        return cudaGetLastError();
+    }
+    // Outputs right behind the states' launch start beside it, on the SMs that it leaves free.
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = pass == LinearPass::kOutputs && !p.seg_ready ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_chunk_kernel<true>, m, a);
 }
 
 }  // namespace kda

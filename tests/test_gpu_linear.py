@@ -243,3 +243,13 @@ def test_long_prompt_single_head(T):
     x = make(1, T, 1, 1, 128, 64, seed=T, mu=-4.0)
     o, hT = kda.linear_fwd(x["q"], x["k"], x["v"], x["log_g"], h0=x["h0"])
     check(x, o, hT)
+
+
+@pytest.mark.parametrize("lens", [[3000, 1, 0, 500], [100] * 40, [1] * 1100, [2000, 0, 3, 2500, 700],
+                                  [0, 0, 5000]], ids=lambda x: "%dx%d" % (len(x), max(x)))
+def test_packed_few_heads(lens):
+    """Documents longer than an SM's share are cut into segments; very many are taken in order."""
+    x = make(1, sum(lens), 1, 1, 32, 64, N=len(lens), seed=len(lens))
+    cu = cu_of(lens)
+    o, hT = kda.linear_fwd(x["q"], x["k"], x["v"], x["log_g"], h0=x["h0"], cu_seqlens=cu)
+    check(x, o, hT, cu)
