@@ -14,9 +14,11 @@
 // one per SM, above). Phases:
 //   load     S by TMA into shared memory, under way until the product; the rows of k and the
 //            gates.
-//   walk     a warp per node i walks i's ancestors with d_ij in registers (4
-//            channels per lane): only products of gates <= 1 appear, so no gate, -inf included,
-//            is out of range. It leaves the two scalars of each pair and the rows k_i d_i, q_i d_i.
+//   paths    d_i of every node in log2(depth) rounds that each double the stretch of path covered.
+//   pairs    d_ij = d_i / d_j, so all pairs are one product [k d; q d] (k / d)^T on the tensor
+//            cores, of which the tree keeps its own. Where some d is below 1e-30 (a gate of -inf
+//            included) the quotient is out of range: then a warp per node walks the node's
+//            ancestors with d_ij in registers, where only products of gates <= 1 appear.
 //   product  [k d; q d] S on the tensor cores (warp-level tf32 products: 16 x 8 x 8). The tree of
 //            bf16 rows uses one tf32 product (its operands lose at most 2^-11 and 2^-10, below the
 //            bf16 output's 2^-8); fp32 rows split both operands into a tf32 part and a tf32
@@ -42,6 +44,8 @@ constexpr int kD = 128;
 constexpr int tree_threads(int nb) { return nb > 2 ? 512 : 256; }
 constexpr int kB = 16;       // nodes per block of the solve
 constexpr int kLd = 136;     // floats per row of the products
+constexpr int kLk = 132;     // floats per row of k: eight rows' fragments in different banks
+constexpr float kSteep = 1e-30f;   // path products below this take the direct walk
 constexpr uint32_t kStateBytes = kD * kD * 4;
 constexpr uint32_t kWaitCycles = 1u << 31;   // about one second
 
@@ -139,6 +143,27 @@ __device__ __forceinline__ void mma_step(float (&c0)[4], float (&c1)[4], float4 
     mma_tf32_16x8x8(c0, ah, b0);
     mma_tf32_16x8x8(c1, ah, b1);
 }
+// One 8-column product.
+template <bool kSplit>
+__device__ __forceinline__ void mma_step(float (&c)[4], float4 f, float p, float q) {
+    if (!kSplit) {
+        const uint32_t a[4] = {__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z),
+                               __float_as_uint(f.w)};
+        const uint32_t b[2] = {__float_as_uint(p), __float_as_uint(q)};
+        mma_tf32_16x8x8(c, a, b);
+        return;
+    }
+    const uint32_t ah[4] = {tf32_rn(f.x), tf32_rn(f.y), tf32_rn(f.z), tf32_rn(f.w)};
+    const uint32_t b[2] = {tf32_rn(p), tf32_rn(q)};
+    const uint32_t al[4] = {
+        tf32_rn(f.x - __uint_as_float(ah[0])), tf32_rn(f.y - __uint_as_float(ah[1])),
+        tf32_rn(f.z - __uint_as_float(ah[2])), tf32_rn(f.w - __uint_as_float(ah[3]))};
+    const uint32_t l[2] = {tf32_rn(p - __uint_as_float(b[0])), tf32_rn(q - __uint_as_float(b[1]))};
+    mma_tf32_16x8x8(c, al, b);
+    mma_tf32_16x8x8(c, ah, l);
+    mma_tf32_16x8x8(c, ah, b);
+}
+
 // Offset of state element (r, c) in shared memory: four 32-column panels as TMA lays them out with
 // the 128-byte swizzle (16-byte pieces permuted by row mod 8).
 __device__ __forceinline__ int state_at(int r, int c) {
@@ -158,27 +183,55 @@ struct TreeSmem {
     static constexpr int kN = kB * NB;
     // S, then the products: rows i of k d S, rows kN + i of q d S
     float state[2 * kN * kLd > kD * kD ? 2 * kN * kLd : kD * kD];
-    float rows[2 * kN * kD];             // k and the gates, then the left operand's fragments
+    float frag[2 * kN * kD];             // the gates, then path products; then the left operand
+    float k[kN * kLk];                   // k, then k / (path product)
     float akk[kN * kN], aqk[kN * kN];    // [j][i]: pairs of node i and j above it (and j = i)
     float u[NB > 1 ? kB * kD : 4];       // the block of u that the blocks behind take
     unsigned long long bad[NB > 1 ? kD : 1];
     unsigned long long above[kN];        // the nodes above each node
-    int par[kN];
+    int par[kN], jump[kN];
     float beta[kN];
     unsigned long long bar;
     int bad_tree;
 };
 
+// Pairs of a tree with steep gates: a warp per node walks the node's ancestors with the product of
+// the gates between in registers, every factor <= 1. The gates come from global memory again.
 template <typename Tin, int NB>
-__global__ void __launch_bounds__(tree_threads(NB), NB <= 2 && sizeof(Tin) == 2 ? 2 : 1)
-decode_tree_kernel(const __grid_constant__ CUtensorMap map, const TreeParams p) {
+__device__ __noinline__ void direct_pairs(TreeSmem<Tin, NB>& sm, const TreeParams& p, int n, int h,
+                                          int warp, int lane) {
+    constexpr int kN = kB * NB, kWarps = tree_threads(NB) / 32;
+    for (int i = (int)threadIdx.x; i < kN * kN / 2; i += 32 * kWarps)   // both matrices
+        *reinterpret_cast<float4*>(sm.akk + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    const Tin* q = static_cast<const Tin*>(p.q);
+    for (int i = warp; i < kN; i += kWarps) {
+        if (sm.par[i] == -2) continue;
+        auto at = [&](int j) { return (((size_t)n * p.T + j) * p.H + h) * kD + 4 * lane; };
+        const float4 ki = load4(sm.k + i * kLk + 4 * lane), qi = load4(q + at(i));
+        float4 d = make_float4(1.f, 1.f, 1.f, 1.f);
+        for (int j = i; j >= 0; j = sm.par[j]) {
+            const float4 kj = mul4(d, load4(sm.k + j * kLk + 4 * lane));
+            const float x[8] = {dot4(ki, kj), dot4(qi, kj), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const float sum = warp_sum8(x, lane);
+            if (lane == 0 && j != i) sm.akk[j * kN + i] = sum;
+            if (lane == 4) sm.aqk[j * kN + i] = sum;
+            const float4 g = load4(p.log_g + at(j));
+            d = mul4(d, make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w)));
+        }
+    }
+}
+
+template <typename Tin, int NB>
+__global__ void __launch_bounds__(tree_threads(NB), NB == 1 && sizeof(Tin) == 2 ? 2 : 1)
+decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
     using Smem = TreeSmem<Tin, NB>;
     constexpr int kN = Smem::kN, kThreads = tree_threads(NB), kWarps = kThreads / 32;
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int unit = blockIdx.x, n = unit / p.H, h = unit % p.H, T = p.T;
-    float *s_k = sm.rows, *s_g = sm.rows + kN * kD;
+    float* s_d = sm.frag;   // the gates, then the products over each node's path
     const Tin* q = static_cast<const Tin*>(p.q);
     const Tin* k = static_cast<const Tin*>(p.k);
     const Tin* v = static_cast<const Tin*>(p.v);
@@ -193,22 +246,39 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const TreeParams p) 
             tma_load_2d(smem_u32(sm.state + i * kD * 32), &map, bar, 32 * i, unit * kD);
         sm.bad_tree = 0;
     }
-    for (int i = tid; i < T * (kD / 4); i += kThreads) {
-        const int r = i >> 5, c = 4 * (i & 31);
-        const float4 g = load4(p.log_g + row(r) + c);
-        *reinterpret_cast<float4*>(s_k + r * kD + c) = load4(k + row(r) + c);
-        *reinterpret_cast<float4*>(s_g + r * kD + c) =
-            make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+    // this thread's pieces: node piece / 32, four channels; absent nodes hold k = q = 0, gate 1
+    constexpr int kMine = kN * 32 / kThreads;
+    float4 qd[kMine], kd[kMine];
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int r = m * kWarps + warp, c = 4 * lane;
+        const bool there = r < T && p.nodes[(size_t)n * T + min(r, T - 1)] != -2;
+        kd[m] = qd[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (there) {
+            kd[m] = load4(k + row(r) + c);
+            qd[m] = load4(q + row(r) + c);
+            const float4 x = load4(p.log_g + row(r) + c);
+            g = make_float4(expf(x.x), expf(x.y), expf(x.z), expf(x.w));
+        }
+        *reinterpret_cast<float4*>(s_d + r * kD + c) = g;
+        *reinterpret_cast<float4*>(sm.k + r * kLk + c) = kd[m];
+    }
+    const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and block of nodes
+    float y[kB], r[kB];
+    if (blk < NB) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) r[i] = load_elem(v, row(min(kB * blk + i, T - 1)) + col);
     }
     if (tid < kN) {
         const int par = tid < T ? p.nodes[(size_t)n * T + tid] : -2;
         sm.par[tid] = par;
+        sm.jump[tid] = par;
+        sm.above[tid] = par >= 0 && par < kN ? 1ull << par : 0;
         sm.beta[tid] = par == -2 ? 0.f
                                  : load_elem(static_cast<const Tin*>(p.beta),
                                              ((int64_t)n * T + tid) * p.H + h);
     }
-    for (int i = tid; i < kN * kN / 2; i += kThreads)   // both matrices
-        *reinterpret_cast<float4*>(sm.akk + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
     if (tid < T) {   // -2: no node; else the root or an earlier node that is there
         const int par = sm.par[tid];
@@ -223,76 +293,88 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const TreeParams p) 
         return;
     }
 
-    // walk: nodes warp, warp + kWarps, ..., two at a time (their chains interleave); their rows
-    // stay in registers until every warp has read k and the gates
-    constexpr int kMine = kN / kWarps;
-    float4 kd[kMine], qd[kMine];
-#pragma unroll
-    for (int b = 0; b < kMine; b += 2) {
-        float4 d[2];
-        int j[2];
-        unsigned long long above[2] = {0, 0};
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const int i = kWarps * (b + w) + warp;
-            j[w] = sm.par[i] != -2 ? i : -1;
-            d[w] = make_float4(1.f, 1.f, 1.f, 1.f);
-            kd[b + w] = qd[b + w] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j[w] >= 0) {
-                kd[b + w] = load4(s_k + i * kD + 4 * lane);
-                qd[b + w] = load4(q + row(i) + 4 * lane);
-            }
-        }
+    // paths: each round multiplies a node's product by that of the node its path has reached, and
+    // reaches twice as far
+    bool steep = false;
 #pragma unroll 1
-        while (j[0] >= 0 || j[1] >= 0) {
-            float x[8];
-            int at[4];   // pair (ancestor m, node w) at 2 m + w
+    for (int far = 1; far < kN; far *= 2) {
+        float4 d[kMine];
+        int to[kMine];
+        unsigned long long above = 0;
+        int jump = -1;
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int e = 2 * m + w;
-                    at[e] = j[w];
-                    x[e] = x[4 + e] = 0.f;
-                    if (j[w] >= 0) {
-                        const float4 kj = mul4(d[w], load4(s_k + j[w] * kD + 4 * lane));
-                        x[e] = dot4(kd[b + w], kj);
-                        x[4 + e] = dot4(qd[b + w], kj);
-                        d[w] = mul4(d[w], load4(s_g + j[w] * kD + 4 * lane));
-                        above[w] |= 1ull << j[w];
-                        j[w] = sm.par[j[w]];
-                    }
-                }
-            const float sum = warp_sum8(x, lane);
-            const int e = lane >> 2 & 3, i = kWarps * (b + (e & 1)) + warp;
-            const int to = e == 0 ? at[0] : e == 1 ? at[1] : e == 2 ? at[2] : at[3];
-            if ((lane & 3) == 0 && to >= 0) {
-                if (lane < 16) sm.akk[to * kN + i] = to == i ? 0.f : sum;
-                else sm.aqk[to * kN + i] = sum;
-            }
+        for (int m = 0; m < kMine; ++m) {
+            const int i = m * kWarps + warp;
+            to[m] = sm.jump[i];
+            if (to[m] >= 0)
+                d[m] = mul4(load4(s_d + i * kD + 4 * lane), load4(s_d + to[m] * kD + 4 * lane));
         }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const int i = kWarps * (b + w) + warp;
-            if (sm.par[i] != -2) {
-                kd[b + w] = mul4(kd[b + w], d[w]);
-                qd[b + w] = mul4(qd[b + w], d[w]);
-            }
-            if (lane == 0) sm.above[i] = above[w] & ~(1ull << i);
+        if (tid < kN && sm.jump[tid] >= 0) {
+            above = sm.above[tid] | sm.above[sm.jump[tid]];
+            jump = sm.jump[sm.jump[tid]];
         }
+        __syncthreads();
+        bool more = false;
+#pragma unroll
+        for (int m = 0; m < kMine; ++m)
+            if (to[m] >= 0) *reinterpret_cast<float4*>(s_d + (m * kWarps + warp) * kD + 4 * lane) = d[m];
+        if (tid < kN && sm.jump[tid] >= 0) {
+            sm.above[tid] = above;
+            sm.jump[tid] = jump;
+            more = jump >= 0;
+        }
+        if (!__syncthreads_or(more)) break;
+    }
+    // the left operand's rows k d and q d; k / d for the pairs
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const float4 d = load4(s_d + (m * kWarps + warp) * kD + 4 * lane);
+        steep |= !(fminf(fminf(d.x, d.y), fminf(d.z, d.w)) >= kSteep);
+        steep |= d.x != d.x || d.y != d.y || d.z != d.z || d.w != d.w;
+        kd[m] = mul4(kd[m], d);
+        qd[m] = mul4(qd[m], d);
+    }
+    steep = __syncthreads_or(steep);
+    if (!steep) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int i = m * kWarps + warp;
+            float4* at = reinterpret_cast<float4*>(sm.k + i * kLk + 4 * lane);
+            const float4 x = *at, d = load4(s_d + i * kD + 4 * lane);
+            *at = make_float4(x.x / d.x, x.y / d.y, x.z / d.z, x.w / d.w);
+        }
+        __syncthreads();
+    } else {
+        direct_pairs<Tin, NB>(sm, p, n, h, warp, lane);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int i = m * kWarps + warp;
+        store_frag<sizeof(Tin) == 2>(sm.frag + (i >> 4) * 2048, i & 15, lane, kd[m]);
+        store_frag<sizeof(Tin) == 2>(sm.frag + (NB + (i >> 4)) * 2048, i & 15, lane, qd[m]);
     }
     __syncthreads();
+    if (!steep) {
+        // pairs: tile (16 rows of [k d; q d]) x (8 nodes)
+#pragma unroll 1
+        for (int tile = warp; tile < 4 * NB * NB; tile += kWarps) {
+            const int mt = tile / (2 * NB), nt = tile % (2 * NB);
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            const float* b = sm.k + (8 * nt + (lane >> 2)) * kLk + (lane & 3);
 #pragma unroll
-    for (int b = 0; b < kMine; ++b) {
-        const int i = kWarps * b + warp;
-        store_frag<sizeof(Tin) == 2>(sm.rows + (i >> 4) * 2048, i & 15, lane, kd[b]);
-        store_frag<sizeof(Tin) == 2>(sm.rows + (NB + (i >> 4)) * 2048, i & 15, lane, qd[b]);
-    }
-    const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and block of nodes
-    float y[kB], r[kB];
-    if (blk < NB) {
+            for (int ks = 0; ks < 16; ++ks)
+                mma_step<sizeof(Tin) == 4>(c, load_frag(sm.frag + mt * 2048, ks, lane), b[8 * ks],
+                                           b[8 * ks + 4]);
+            float* to = mt < NB ? sm.akk : sm.aqk;
 #pragma unroll
-        for (int i = 0; i < kB; ++i) r[i] = load_elem(v, row(min(kB * blk + i, T - 1)) + col);
+            for (int e = 0; e < 4; ++e) {   // rows g, g + 8; nodes 2 t, 2 t + 1
+                const int i = 16 * (mt % NB) + (lane >> 2) + 8 * (e >> 1);
+                const int j = 8 * nt + 2 * (lane & 3) + (e & 1);
+                const bool pair = (sm.above[i] >> j & 1) || (mt >= NB && i == j);
+                to[j * kN + i] = pair ? c[e] : 0.f;
+            }
+        }
     }
     const bool ok = mbar_wait(bar, 0, kWaitCycles);
     if (!ok) set_device_error(p.err, DEV_TIMEOUT);
@@ -301,7 +383,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const TreeParams p) 
     {   // product: 16 columns per warp; all 2 NB tiles, or k d and q d by 8 warps each
         constexpr int kTiles = 2 * NB / (kWarps / 8);
         const int cols = 16 * (warp & 7), t0 = (warp >> 3) * kTiles;
-        const float* frag = sm.rows + t0 * 2048;
+        const float* frag = sm.frag + t0 * 2048;
         const int at0 = state_at(lane & 3, cols + 2 * (lane >> 2));
         const int at1 = state_at((lane & 3) + 4, cols + 2 * (lane >> 2));
         float c0[kTiles][4], c1[kTiles][4];
@@ -324,11 +406,6 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const TreeParams p) 
     }
     __syncthreads();
 
-    // The pairs of other branches have coefficient 0. An infinite or NaN u would turn that into
-    // NaN, so such a u enters the sums as 0, and `bad` has its node: what is below it in the tree
-    // becomes NaN, what is beside it does not.
-    unsigned long long bad = 0;
-    Tin* o = static_cast<Tin*>(p.o);
     if (blk < NB) {
 #pragma unroll
         for (int i = 0; i < kB; ++i) {
@@ -336,59 +413,76 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const TreeParams p) 
             y[i] = sm.state[(kN + kB * blk + i) * kLd + col];
         }
     }
+    // r and y less what node (b, j)'s u adds to the rows e of block `to`, first <= e
+    auto spread = [&](int at, int to, float u, int first) {
+        const float *ak = sm.akk + at * kN + kB * to, *aq = sm.aqk + at * kN + kB * to;
+#pragma unroll
+        for (int i4 = 0; i4 < kB; i4 += 4) {
+            if (i4 + 3 < first) continue;
+            const float4 a = load4(ak + i4), c = load4(aq + i4);
+            const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i4 + e >= first) {
+                    r[i4 + e] = fmaf(-av[e], u, r[i4 + e]);
+                    y[i4 + e] = fmaf(cv[e], u, y[i4 + e]);
+                }
+        }
+    };
+    Tin* o = static_cast<Tin*>(p.o);
+    unsigned long long bad = 0;   // nodes whose u is infinite or NaN in this column
     for (int b = 0; b < NB; ++b) {
         if (blk == b) {
             if (NB > 1 && b > 0) bad = sm.bad[col];
+            float finite = 0.f;
+            float* rs = sm.state + kB * b * kLd + col;           // r and y as they are, kept in
+            float* ys = sm.state + (kN + kB * b) * kLd + col;    // the products' places
+#pragma unroll
+            for (int j = 0; j < kB; ++j) rs[j * kLd] = r[j], ys[j * kLd] = y[j];
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
                 const int at = kB * b + j;
-                const bool below = bad & sm.above[at];
-                float u = below ? __int_as_float(0x7fc00000) : sm.beta[at] * r[j];
-                const float* ak = sm.akk + at * kN + kB * b;
-                const float* aq = sm.aqk + at * kN + kB * b;
-                y[j] = fmaf(aq[j], u, y[j]);
-                if (!(fabsf(u) <= 3.402823466e38f)) {
-                    u = 0.f;
-                    bad |= 1ull << at;
-                }
-#pragma unroll
-                for (int i4 = 0; i4 < kB; i4 += 4) {
-                    if (i4 + 3 <= j) continue;
-                    const float4 a = load4(ak + i4), c = load4(aq + i4);
-                    const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (i4 + e > j) {
-                            r[i4 + e] = fmaf(-av[e], u, r[i4 + e]);
-                            y[i4 + e] = fmaf(cv[e], u, y[i4 + e]);
-                        }
-                }
+                const float u = sm.beta[at] * r[j];
+                finite = fmaf(u, 0.f, finite);
+                y[j] = fmaf(sm.aqk[at * kN + at], u, y[j]);
+                spread(at, b, u, j + 1);
                 if (NB > 1) sm.u[j * kD + col] = u;
             }
+            if (bad != 0 || finite != 0.f) {
+                // The pairs of other branches have coefficient 0. An infinite or NaN u turned that
+                // into NaN: again, with such a u entering the sums as 0. What is below its node in
+                // the tree becomes NaN, what is beside it does not.
+#pragma unroll 1
+                for (int j = 0; j < kB; ++j) {
+                    const int at = kB * b + j;
+                    const float *ak = sm.akk + at * kN + kB * b, *aq = sm.aqk + at * kN + kB * b;
+                    float u = bad & sm.above[at] ? __int_as_float(0x7fc00000)
+                                                 : sm.beta[at] * rs[j * kLd];
+                    ys[j * kLd] = fmaf(aq[j], u, ys[j * kLd]);
+                    if (!(fabsf(u) <= 3.402823466e38f)) {
+                        u = 0.f;
+                        bad |= 1ull << at;
+                    }
+                    if (NB > 1) sm.u[j * kD + col] = u;
+#pragma unroll 1
+                    for (int e = j + 1; e < kB; ++e) {
+                        rs[e * kLd] = fmaf(-ak[e], u, rs[e * kLd]);
+                        ys[e * kLd] = fmaf(aq[e], u, ys[e * kLd]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kB; ++j) y[j] = ys[j * kLd];
+            }
+            if (NB > 1) sm.bad[col] = bad;
 #pragma unroll
             for (int j = 0; j < kB; ++j)
                 if (sm.par[kB * b + j] != -2) store_elem(o, row(kB * b + j) + col, y[j]);
-            if (NB > 1) sm.bad[col] = bad;
         }
         if (NB > 1 && b + 1 < NB) {
             __syncthreads();
             if (blk > b && blk < NB) {
 #pragma unroll 4
-                for (int j = 0; j < kB; ++j) {
-                    const float u = sm.u[j * kD + col];
-                    const float* ak = sm.akk + (kB * b + j) * kN + kB * blk;
-                    const float* aq = sm.aqk + (kB * b + j) * kN + kB * blk;
-#pragma unroll
-                    for (int i4 = 0; i4 < kB; i4 += 4) {
-                        const float4 a = load4(ak + i4), c = load4(aq + i4);
-                        const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            r[i4 + e] = fmaf(-av[e], u, r[i4 + e]);
-                            y[i4 + e] = fmaf(cv[e], u, y[i4 + e]);
-                        }
-                    }
-                }
+                for (int j = 0; j < kB; ++j) spread(kB * b + j, blk, sm.u[j * kD + col], 0);
             }
             __syncthreads();
         }

@@ -256,3 +256,16 @@ def test_refusals():
     with pytest.raises(ValueError):
         kda.commit_path(x["k"], x["v"], x["log_g"], x["beta"], P[:1], x["S"])
     assert kda.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [7, 30, 64])
+@pytest.mark.parametrize("gate", [-3.0, -30.0, -90.0])
+def test_tree_chains_near_the_range(T, gate, dtype):
+    """Paths whose gate products approach and pass what a float's range holds."""
+    x = make(1, T, 2, dtype, seed=T)
+    x["log_g"][:, ::4] = gate
+    parents = random_parents(1, T, 5, "chain")
+    o = kda.decode_tree(x["q"], x["k"], x["v"], x["log_g"], x["beta"],
+                        torch.tensor(parents, device=DEV), x["S"])
+    check_tree(x, parents, o, torch.zeros_like(o))
