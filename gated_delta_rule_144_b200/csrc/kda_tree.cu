@@ -188,8 +188,8 @@ struct TreeSmem {
     float akk[kN * kN], aqk[kN * kN];    // [j][i]: pairs of node i and j above it (and j = i)
     float u[NB > 1 ? kB * kD : 4];       // the block of u that the blocks behind take
     unsigned long long bad[NB > 1 ? kD : 1];
-    unsigned long long above[kN];        // the nodes above each node
-    int par[kN], jump[kN];
+    unsigned long long above[2][kN];     // the nodes above each node
+    int par[kN], jump[2][kN];
     float beta[kN];
     unsigned long long bar;
     int bad_tree;
@@ -238,31 +238,40 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     auto row = [&](int i) { return (((size_t)n * T + i) * p.H + h) * kD; };
     const uint32_t bar = smem_u32(&sm.bar);
 
-    if (tid == 0) {
-        mbar_init(bar, 1);
-        fence_mbar_init();
-        mbar_arrive_expect_tx(bar, kStateBytes);
-        for (int i = 0; i < 4; ++i)
-            tma_load_2d(smem_u32(sm.state + i * kD * 32), &map, bar, 32 * i, unit * kD);
-        sm.bad_tree = 0;
-    }
     // this thread's pieces: node piece / 32, four channels; absent nodes hold k = q = 0, gate 1
     constexpr int kMine = kN * 32 / kThreads;
     float4 qd[kMine], kd[kMine];
+    {   // (loads that wait for nothing; rows of absent nodes are dropped afterwards)
+        float4 g[kMine];
+        int par[kMine];
 #pragma unroll
-    for (int m = 0; m < kMine; ++m) {
-        const int r = m * kWarps + warp, c = 4 * lane;
-        const bool there = r < T && p.nodes[(size_t)n * T + min(r, T - 1)] != -2;
-        kd[m] = qd[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (there) {
-            kd[m] = load4(k + row(r) + c);
-            qd[m] = load4(q + row(r) + c);
-            const float4 x = load4(p.log_g + row(r) + c);
-            g = make_float4(expf(x.x), expf(x.y), expf(x.z), expf(x.w));
+        for (int m = 0; m < kMine; ++m) {
+            const int r = min(m * kWarps + warp, T - 1);
+            kd[m] = load4(k + row(r) + 4 * lane);
+            qd[m] = load4(q + row(r) + 4 * lane);
+            g[m] = load4(p.log_g + row(r) + 4 * lane);
+            par[m] = p.nodes[(size_t)n * T + r];
         }
-        *reinterpret_cast<float4*>(s_d + r * kD + c) = g;
-        *reinterpret_cast<float4*>(sm.k + r * kLk + c) = kd[m];
+        if (tid == 0) {   // behind the rows, which are needed first
+            mbar_init(bar, 1);
+            fence_mbar_init();
+            mbar_arrive_expect_tx(bar, kStateBytes);
+            for (int i = 0; i < 4; ++i)
+                tma_load_2d(smem_u32(sm.state + i * kD * 32), &map, bar, 32 * i, unit * kD);
+            sm.bad_tree = 0;
+        }
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int r = m * kWarps + warp;
+            if (r >= T || par[m] == -2) {
+                kd[m] = qd[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+                g[m] = make_float4(1.f, 1.f, 1.f, 1.f);
+            } else {
+                g[m] = make_float4(expf(g[m].x), expf(g[m].y), expf(g[m].z), expf(g[m].w));
+            }
+            *reinterpret_cast<float4*>(s_d + r * kD + 4 * lane) = g[m];
+            *reinterpret_cast<float4*>(sm.k + r * kLk + 4 * lane) = kd[m];
+        }
     }
     const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and block of nodes
     float y[kB], r[kB];
@@ -273,8 +282,8 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     if (tid < kN) {
         const int par = tid < T ? p.nodes[(size_t)n * T + tid] : -2;
         sm.par[tid] = par;
-        sm.jump[tid] = par;
-        sm.above[tid] = par >= 0 && par < kN ? 1ull << par : 0;
+        sm.jump[0][tid] = par;
+        sm.above[0][tid] = par >= 0 && par < kN ? 1ull << par : 0;
         sm.beta[tid] = par == -2 ? 0.f
                                  : load_elem(static_cast<const Tin*>(p.beta),
                                              ((int64_t)n * T + tid) * p.H + h);
@@ -294,41 +303,39 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     }
 
     // paths: each round multiplies a node's product by that of the node its path has reached, and
-    // reaches twice as far
+    // reaches twice as far (two places for the products and the jumps, taken in turn)
     bool steep = false;
+    int at = 0;
 #pragma unroll 1
-    for (int far = 1; far < kN; far *= 2) {
-        float4 d[kMine];
-        int to[kMine];
-        unsigned long long above = 0;
-        int jump = -1;
+    for (bool more = true; more; at ^= 1) {
+        const float* from = s_d + at * kN * kD;
+        float* to = s_d + (at ^ 1) * kN * kD;
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const int i = m * kWarps + warp;
-            to[m] = sm.jump[i];
-            if (to[m] >= 0)
-                d[m] = mul4(load4(s_d + i * kD + 4 * lane), load4(s_d + to[m] * kD + 4 * lane));
+            const int i = m * kWarps + warp, j = sm.jump[at][i];
+            float4 d = load4(from + i * kD + 4 * lane);
+            if (j >= 0) d = mul4(d, load4(from + j * kD + 4 * lane));
+            *reinterpret_cast<float4*>(to + i * kD + 4 * lane) = d;
         }
-        if (tid < kN && sm.jump[tid] >= 0) {
-            above = sm.above[tid] | sm.above[sm.jump[tid]];
-            jump = sm.jump[sm.jump[tid]];
+        int far = -1;
+        if (tid < kN) {
+            const int j = sm.jump[at][tid];
+            unsigned long long above = sm.above[at][tid];
+            if (j >= 0) {
+                above |= sm.above[at][j];
+                far = sm.jump[at][j];
+            }
+            sm.jump[at ^ 1][tid] = far;
+            sm.above[at ^ 1][tid] = above;
         }
-        __syncthreads();
-        bool more = false;
-#pragma unroll
-        for (int m = 0; m < kMine; ++m)
-            if (to[m] >= 0) *reinterpret_cast<float4*>(s_d + (m * kWarps + warp) * kD + 4 * lane) = d[m];
-        if (tid < kN && sm.jump[tid] >= 0) {
-            sm.above[tid] = above;
-            sm.jump[tid] = jump;
-            more = jump >= 0;
-        }
-        if (!__syncthreads_or(more)) break;
+        more = __syncthreads_or(far >= 0);
     }
+    const float* path = s_d + at * kN * kD;
+    const unsigned long long* s_above = sm.above[at];
     // the left operand's rows k d and q d; k / d for the pairs
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
-        const float4 d = load4(s_d + (m * kWarps + warp) * kD + 4 * lane);
+        const float4 d = load4(path + (m * kWarps + warp) * kD + 4 * lane);
         steep |= !(fminf(fminf(d.x, d.y), fminf(d.z, d.w)) >= kSteep);
         steep |= d.x != d.x || d.y != d.y || d.z != d.z || d.w != d.w;
         kd[m] = mul4(kd[m], d);
@@ -339,9 +346,9 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
             const int i = m * kWarps + warp;
-            float4* at = reinterpret_cast<float4*>(sm.k + i * kLk + 4 * lane);
-            const float4 x = *at, d = load4(s_d + i * kD + 4 * lane);
-            *at = make_float4(x.x / d.x, x.y / d.y, x.z / d.z, x.w / d.w);
+            float4* to = reinterpret_cast<float4*>(sm.k + i * kLk + 4 * lane);
+            const float4 x = *to, d = load4(path + i * kD + 4 * lane);
+            *to = make_float4(x.x / d.x, x.y / d.y, x.z / d.z, x.w / d.w);
         }
         __syncthreads();
     } else {
@@ -355,14 +362,57 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
         store_frag<sizeof(Tin) == 2>(sm.frag + (NB + (i >> 4)) * 2048, i & 15, lane, qd[m]);
     }
     __syncthreads();
-    if (!steep) {
-        // pairs: tile (16 rows of [k d; q d]) x (8 nodes)
+    const bool ok = mbar_wait(bar, 0, kWaitCycles);
+    if (!ok) set_device_error(p.err, DEV_TIMEOUT);
+    if (__syncthreads_or(!ok)) return;
+
+    // half of the warps take the products with S (all 2 NB tiles of their columns, so that S is read
+    // once), the others the pairs
+    if (warp < kWarps / 2) {
+        constexpr int kCols = kD / (kWarps / 2), kN8 = kCols / 16;   // columns, pairs of 8 of them
+        const int cols = kCols * warp;
+        int at0[kN8], at1[kN8];
+#pragma unroll
+        for (int e = 0; e < kN8; ++e) {
+            at0[e] = state_at(lane & 3, cols + 16 * e + 2 * (lane >> 2));
+            at1[e] = state_at((lane & 3) + 4, cols + 16 * e + 2 * (lane >> 2));
+        }
+        float c0[2 * NB][kN8][4], c1[2 * NB][kN8][4];
+#pragma unroll
+        for (int b = 0; b < 2 * NB; ++b)
+#pragma unroll
+            for (int e = 0; e < kN8; ++e)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) c0[b][e][x] = c1[b][e][x] = 0.f;
+#pragma unroll 2
+        for (int ks = 0; ks < 16; ++ks) {
+            float2 s0[kN8], s1[kN8];
+#pragma unroll
+            for (int e = 0; e < kN8; ++e) {
+                s0[e] = *reinterpret_cast<const float2*>(sm.state + at0[e] + ks * 256);
+                s1[e] = *reinterpret_cast<const float2*>(sm.state + at1[e] + ks * 256);
+            }
+#pragma unroll
+            for (int b = 0; b < 2 * NB; ++b) {
+                const float4 f = load_frag(sm.frag + b * 2048, ks, lane);
+#pragma unroll
+                for (int e = 0; e < kN8; ++e)
+                    mma_step<sizeof(Tin) == 4>(c0[b][e], c1[b][e], f, s0[e], s1[e]);
+            }
+        }
+        bar_sync(1, kThreads / 2);   // S has been read
+#pragma unroll
+        for (int b = 0; b < 2 * NB; ++b)
+#pragma unroll
+            for (int e = 0; e < kN8; ++e)
+                store_tile(sm.state + kB * b * kLd, cols + 16 * e, lane, c0[b][e], c1[b][e]);
+    } else if (!steep) {   // tile (16 rows of [k d; q d]) x (8 nodes)
 #pragma unroll 1
-        for (int tile = warp; tile < 4 * NB * NB; tile += kWarps) {
+        for (int tile = warp - kWarps / 2; tile < 4 * NB * NB; tile += kWarps / 2) {
             const int mt = tile / (2 * NB), nt = tile % (2 * NB);
             float c[4] = {0.f, 0.f, 0.f, 0.f};
             const float* b = sm.k + (8 * nt + (lane >> 2)) * kLk + (lane & 3);
-#pragma unroll
+#pragma unroll 4
             for (int ks = 0; ks < 16; ++ks)
                 mma_step<sizeof(Tin) == 4>(c, load_frag(sm.frag + mt * 2048, ks, lane), b[8 * ks],
                                            b[8 * ks + 4]);
@@ -371,38 +421,10 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             for (int e = 0; e < 4; ++e) {   // rows g, g + 8; nodes 2 t, 2 t + 1
                 const int i = 16 * (mt % NB) + (lane >> 2) + 8 * (e >> 1);
                 const int j = 8 * nt + 2 * (lane & 3) + (e & 1);
-                const bool pair = (sm.above[i] >> j & 1) || (mt >= NB && i == j);
+                const bool pair = (s_above[i] >> j & 1) || (mt >= NB && i == j);
                 to[j * kN + i] = pair ? c[e] : 0.f;
             }
         }
-    }
-    const bool ok = mbar_wait(bar, 0, kWaitCycles);
-    if (!ok) set_device_error(p.err, DEV_TIMEOUT);
-    if (__syncthreads_or(!ok)) return;
-
-    {   // product: 16 columns per warp; all 2 NB tiles, or k d and q d by 8 warps each
-        constexpr int kTiles = 2 * NB / (kWarps / 8);
-        const int cols = 16 * (warp & 7), t0 = (warp >> 3) * kTiles;
-        const float* frag = sm.frag + t0 * 2048;
-        const int at0 = state_at(lane & 3, cols + 2 * (lane >> 2));
-        const int at1 = state_at((lane & 3) + 4, cols + 2 * (lane >> 2));
-        float c0[kTiles][4], c1[kTiles][4];
-#pragma unroll
-        for (int b = 0; b < kTiles; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c0[b][e] = c1[b][e] = 0.f;
-#pragma unroll 4
-        for (int ks = 0; ks < 16; ++ks) {
-            const float2 s0 = *reinterpret_cast<const float2*>(sm.state + at0 + ks * 256);
-            const float2 s1 = *reinterpret_cast<const float2*>(sm.state + at1 + ks * 256);
-#pragma unroll
-            for (int b = 0; b < kTiles; ++b)
-                mma_step<sizeof(Tin) == 4>(c0[b], c1[b], load_frag(frag + b * 2048, ks, lane), s0, s1);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int b = 0; b < kTiles; ++b)
-            store_tile(sm.state + kB * (t0 + b) * kLd, cols, lane, c0[b], c1[b]);
     }
     __syncthreads();
 
@@ -456,7 +478,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
                 for (int j = 0; j < kB; ++j) {
                     const int at = kB * b + j;
                     const float *ak = sm.akk + at * kN + kB * b, *aq = sm.aqk + at * kN + kB * b;
-                    float u = bad & sm.above[at] ? __int_as_float(0x7fc00000)
+                    float u = bad & s_above[at] ? __int_as_float(0x7fc00000)
                                                  : sm.beta[at] * rs[j * kLd];
                     ys[j * kLd] = fmaf(aq[j], u, ys[j * kLd]);
                     if (!(fabsf(u) <= 3.402823466e38f)) {
