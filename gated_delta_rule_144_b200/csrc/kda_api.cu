@@ -807,7 +807,7 @@ static int linear_walk_segment(const kda_linear_desc_t* d) {
 // Tokens per segment of the chunked kernel (0: whole sequences), whose CTAs take one (segment,
 // head, 64 value columns) each, one per SM. Equal lengths: the count of segments with the least
 // modelled time, in units of one chunk with outputs (about 2 us): waves of m such chunks, and
-// before them the states of all segments but the last at 0.65 of a chunk each, 3 units per CTA's
+// before them the states of all segments but the last at 0.4 of a chunk each, 3 units per CTA's
 // start and end, 1 for the further launch. Packed documents, whose lengths the host does not see,
 // are cut only where one takes much more than an SM's even share of all chunks (the CTAs take the
 // longest first, so shorter ones pack well).
@@ -824,7 +824,7 @@ static int linear_chunk_segment(const kda_linear_desc_t* d, bool packed) {
     for (int m = 1; m < n; ++m) {
         const int P = (n + m - 1) / m;
         if (P > 64) continue;
-        const double cost = std::ceil(all * (P - 1) / sms) * (0.65 * m + 3.0) +
+        const double cost = std::ceil(all * (P - 1) / sms) * (0.4 * m + 3.0) +
                             std::ceil(all * P / sms) * (m + 3.0) + 1.0;
         if (cost < best) best = cost, m_best = m;
     }

@@ -29,7 +29,8 @@
 //   warps 4-7   state: lane i holds row i of S, 64 columns in registers; adds a chunk's
 //               partial products and writes S as bf16 to shared memory for the next Q S
 //   warps 8-11  values: the three terms of the decayed V to shared memory, 32 rows at a time in
-//               two buffers, so that one is written while the other is multiplied
+//               two buffers, so that one is written while the other is multiplied (without
+//               outputs warps 0-3 take half of them, in four buffers)
 //   warp 12     loader: q, k, v by TMA, two stages. It clears the rows of k and v behind a
 //               sequence's end (they are another's), so that nothing of them enters a product
 //   warp 13     issues the state's products, warp 14 the scores', Q S and P V
@@ -65,13 +66,14 @@ constexpr uint32_t kPanel = 16384;      // 128 rows x 128 bytes, 128-byte swizzl
 constexpr uint32_t ST_Q = 0, ST_K = 2 * kPanel, ST_V = 4 * kPanel, kStage = 5 * kPanel;
 constexpr uint32_t kQuarter = kPanel / 4;           // 32 rows of one term of the decayed V
 constexpr uint32_t kVH = 3 * kQuarter;
-constexpr uint32_t OFF_VH = 2 * kStage;             // two buffers of 32 rows of the three terms
+constexpr uint32_t OFF_VH = 2 * kStage;             // two buffers of 32 rows of the three terms (four
+                                                    // without outputs: also what follows)
 constexpr uint32_t OFF_SB = OFF_VH + 2 * kVH;       // bf16 state
 constexpr uint32_t OFF_OUT = OFF_SB + kPanel;       // output on its way to global memory
 constexpr uint32_t OFF_GATE = OFF_OUT + kPanel;      // per stage: loc[128], suf[128], tot[4]
 constexpr uint32_t kGateBytes = (2 * kC + 4) * 4;
 constexpr uint32_t OFF_BAR = OFF_GATE + 2 * kGateBytes;
-constexpr uint32_t OFF_MISC = OFF_BAR + 26 * 8;     // TMEM address, abort flag
+constexpr uint32_t OFF_MISC = OFF_BAR + 34 * 8;     // TMEM address, abort flag
 constexpr uint32_t kSmem = OFF_MISC + 16;
 static_assert(kSmem <= 232448, "shared memory");
 static_assert(OFF_BAR % 8 == 0 && OFF_GATE % 16 == 0 && kGateBytes % 16 == 0, "alignment");
@@ -249,12 +251,14 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     if (!kOut && sl.last) return;
     const int nchunks = (int)((sl.end - sl.begin + kC - 1) / kC);
     const int j0 = tile * kNV;
+    constexpr int kBufs = kOut ? 2 : 4;
 
-    // barriers: each counts the chunks (pairs: one per stage, or per buffer of b_vh)
+    // barriers: each counts the chunks (pairs: one per stage or parity; b_vh: one per
+    // buffer)
     const uint32_t nb = sb + OFF_BAR;
     const uint32_t b_full = nb, b_qkfree = nb + 16, b_vfree = nb + 32, b_gfull = nb + 48,
-                   b_gfree = nb + 64, b_vh = nb + 80, b_vhfree = nb + 192, b_kv = nb + 104,
-                   b_kvfree = nb + 112, b_p = nb + 120, b_pb = nb + 128, b_s = nb + 136,
+                   b_gfree = nb + 64, b_vh = nb + 208, b_vhfree = nb + 240, b_kv = nb + 80,
+                   b_kvfree = nb + 96, b_p = nb + 120, b_pb = nb + 128, b_s = nb + 136,
                    b_sfree = nb + 144, b_o = nb + 152, b_ofree = nb + 160, b_tail = nb + 168,
                    b_vfull = nb + 176;
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(sm + OFF_MISC);
@@ -265,12 +269,14 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             mbar_init(b_qkfree + 8 * i, kOut ? 2 : 1);    // both issuing warps have read
             mbar_init(b_vfree + 8 * i, 1);
             mbar_init(b_gfull + 8 * i, 1);
-            mbar_init(b_gfree + 8 * i, kOut ? 12 : 8);    // one per reading warp
+            mbar_init(b_gfree + 8 * i, 12);               // one per reading warp
+            mbar_init(b_kv + 8 * i, 1);
+            mbar_init(b_kvfree + 8 * i, 128);
+        }
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(b_vh + 8 * i, 128);
             mbar_init(b_vhfree + 8 * i, 1);
         }
-        mbar_init(b_kv, 1);
-        mbar_init(b_kvfree, 128);
         mbar_init(b_p, 1);
         mbar_init(b_pb, 128);
         mbar_init(b_s, 128);
@@ -306,9 +312,68 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     auto gates = [&](int c) {
         return reinterpret_cast<float*>(sm + OFF_GATE + (c & 1) * kGateBytes);
     };
+    // a chunk's state terms in TMEM: alternating places where nothing else needs them
+    auto kv_at = [&](int c) { return tbase + (kOut || !(c & 1) ? TM_KV : 0u); };
+
+    // The values' role: the decayed V of the 32-row quarters q0, q0 + kStep, ...: lane r takes row r,
+    // the warp 16 of the columns.
+    constexpr int kStep = kOut ? 1 : 2;
+    auto values = [&](int q0) {
+        const int v0 = 2 * (warp & 3);   // first 16-byte piece
+#pragma unroll 1
+        for (int c = 0; c < nchunks; ++c) {
+            if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
+            const float* gt = gates(c);
+            float ek[4], behind = 1.f;
+#pragma unroll
+            for (int q = 3; q >= 0; --q) {
+                ek[q] = behind * gt[kC + 32 * q + lane];
+                behind *= ex2(gt[2 * kC + q]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
+            if (!wait(b_vfull + 8 * (c & 1), c >> 1)) break;
+            const uint8_t* v = sm + (c & 1) * kStage + ST_V + lane * 128;
+            bool ok = true;
+#pragma unroll 1
+            for (int q = q0; q < 4; q += kStep) {
+                // a buffer's use u follows the product that read use u - 1
+                const int b = q & (kBufs - 1), u = kOut ? 2 * c + (q >> 1) : c;
+                ok = u == 0 || wait(b_vhfree + 8 * b, u - 1);
+                if (!ok) break;
+                uint8_t* vh = sm + OFF_VH + b * kVH + lane * 128;
+                const float f = q < 2 ? (q == 0 ? ek[0] : ek[1]) : (q == 2 ? ek[2] : ek[3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t ch = (uint32_t)((v0 + i) ^ (lane & 7)) << 4;
+                    const uint4 x = *reinterpret_cast<const uint4*>(v + q * kQuarter + ch);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t t[3][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a = lo_bf(in[e]), b = hi_bf(in[e]);
+                        mul2(a, b, f);
+#pragma unroll
+                        for (int m = 0; m < 3; ++m) {
+                            t[m][e] = pack2(a, b);
+                            if (m < 2) sub2(a, b, lo_bf(t[m][e]), hi_bf(t[m][e]));
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        *reinterpret_cast<uint4*>(vh + m * kQuarter + ch) =
+                            make_uint4(t[m][0], t[m][1], t[m][2], t[m][3]);
+                }
+                fence_proxy_async();
+                mbar_arrive(b_vh + 8 * b);
+            }
+            if (!ok) break;
+        }
+    };
 
     if (warp < 4) {
         // ============================================================ scores
+        if (!kOut) values(0);
         // chunk c's scores, then, while chunk c + 1's are multiplied, chunk c - 1's output
         const uint32_t pb = tbase + lq + TM_PB;
         float er_last = 0.f;
@@ -478,20 +543,20 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             decay += sum;
             __syncwarp();
             if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
-            if (!wait(b_kv, c)) break;
+            if (!wait(b_kv + 8 * (c & 1), c >> 1)) break;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float x[16], y[16];
-                tmem_ld16(tbase + lq + TM_KV + 16 * q, x);
-                tmem_ld16(tbase + lq + TM_KV + 64 + 16 * q, y);
+                tmem_ld16(kv_at(c) + lq + 16 * q, x);
+                tmem_ld16(kv_at(c) + lq + 64 + 16 * q, y);
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     S[16 * q + i] = fmaf(e, S[16 * q + i], x[i] + y[i]);
             }
             tc_fence_before();
-            mbar_arrive(b_kvfree);
+            mbar_arrive(b_kvfree + 8 * (c & 1));
             if (kOut && c + 1 < nchunks) {
                 if (!wait(b_sfree, c)) break;
                 publish();
@@ -509,58 +574,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         if (!kOut && tile == 0 && row == 0) p.seg_decay[(size_t)sl.slot * p.H + h] = exp2f(decay);
     } else if (warp < 12) {
         // ============================================================ values
-        // 32 rows at a time: lane r takes row r of a quarter, the warp 16 of the columns
-        const int v0 = 2 * (warp & 3);   // first 16-byte piece
-#pragma unroll 1
-        for (int c = 0; c < nchunks; ++c) {
-            if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
-            const float* gt = gates(c);
-            float ek[4], behind = 1.f;
-#pragma unroll
-            for (int q = 3; q >= 0; --q) {
-                ek[q] = behind * gt[kC + 32 * q + lane];
-                behind *= ex2(gt[2 * kC + q]);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
-            if (!wait(b_vfull + 8 * (c & 1), c >> 1)) break;
-            const uint8_t* v = sm + (c & 1) * kStage + ST_V + lane * 128;
-            bool ok = true;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                // a buffer's use u = 2 c + q / 2 follows the product that read use u - 1
-                const int u = 2 * c + (q >> 1);
-                ok = u == 0 || wait(b_vhfree + 8 * (q & 1), u - 1);
-                if (!ok) break;
-                uint8_t* vh = sm + OFF_VH + (q & 1) * kVH + lane * 128;
-                const float f = ek[0];
-                ek[0] = ek[1], ek[1] = ek[2], ek[2] = ek[3];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t ch = (uint32_t)((v0 + i) ^ (lane & 7)) << 4;
-                    const uint4 x = *reinterpret_cast<const uint4*>(v + q * kQuarter + ch);
-                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t t[3][4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float a = lo_bf(in[e]), b = hi_bf(in[e]);
-                        mul2(a, b, f);
-#pragma unroll
-                        for (int m = 0; m < 3; ++m) {
-                            t[m][e] = pack2(a, b);
-                            if (m < 2) sub2(a, b, lo_bf(t[m][e]), hi_bf(t[m][e]));
-                        }
-                    }
-#pragma unroll
-                    for (int m = 0; m < 3; ++m)
-                        *reinterpret_cast<uint4*>(vh + m * kQuarter + ch) =
-                            make_uint4(t[m][0], t[m][1], t[m][2], t[m][3]);
-                }
-                fence_proxy_async();
-                mbar_arrive(b_vh + 8 * (q & 1));
-            }
-            if (!ok) break;
-        }
+        values(kOut ? 0 : 1);
     } else if (warp == kLoadWarp) {
         // ============================================================ loader
         // Loads of a chunk follow its stage's release, a chunk before their use; its tiles are
@@ -638,33 +652,41 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
 #pragma unroll 1
         for (; c < nchunks; ++c) {
             uint32_t k = sb + (c & 1) * kStage + ST_K;
-            ok = wait(b_full + 8 * (c & 1), c >> 1) && (c == 0 || wait(b_kvfree, c - 1));
+            // (kOut: one place for the terms, free once chunk c - 1's were read; else c - 2's)
+            const int before = c - (kOut ? 1 : 2);
+            ok = wait(b_full + 8 * (c & 1), c >> 1) &&
+                 (before < 0 || wait(b_kvfree + 8 * (before & 1), before >> 1));
+            const uint32_t kv = kv_at(c);
 #pragma unroll 1
             for (int q = 0; ok && q < 4; ++q) {
-                ok = wait(b_vh + 8 * (q & 1), 2 * c + (q >> 1));
+                const int b = q & (kBufs - 1);
+                ok = wait(b_vh + 8 * b, kOut ? 2 * c + (q >> 1) : c);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t v = sb + OFF_VH + (q & 1) * kVH;
+                uint32_t v = sb + OFF_VH + b * kVH;
                 // the first two terms side by side, then the third onto the second's sum
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    umma_f16_warp(tbase + TM_KV, desc_at(dM, k), desc_at(dV, v), id2, q > 0 || s > 0);
-                    umma_f16_warp(tbase + TM_KV + kNV, desc_at(dM, k), desc_at(dV, v + 2 * kQuarter),
+                    umma_f16_warp(kv, desc_at(dM, k), desc_at(dV, v), id2, q > 0 || s > 0);
+                    umma_f16_warp(kv + kNV, desc_at(dM, k), desc_at(dV, v + 2 * kQuarter),
                                   id1, 1);
                     k += 2048;
                     v += 2048;
                 }
-                umma_commit_warp(b_vhfree + 8 * (q & 1));
+                umma_commit_warp(b_vhfree + 8 * b);
             }
             if (!ok) break;
-            umma_commit_warp(b_kv);
+            umma_commit_warp(b_kv + 8 * (c & 1));
             umma_commit_warp(b_qkfree + 8 * (c & 1));
             if (!kOut) umma_commit_warp(b_vfree + 8 * (c & 1));
         }
         // every product issued is finished before TMEM and the shared memory go away: the last
         // chunk's, or, on the way out after an expired wait, what this last commit covers
-        if (c < nchunks) umma_commit_warp(b_kv);
-        if (nchunks > 0) wait_phase(b_kv, (uint32_t)(min(c, nchunks - 1) & 1), args.budget);
+        if (c < nchunks) umma_commit_warp(b_kv + 8 * (c & 1));
+        if (nchunks > 0) {
+            const int last = min(c, nchunks - 1);
+            wait_phase(b_kv + 8 * (last & 1), (uint32_t)((last >> 1) & 1), args.budget);
+        }
     } else if (warp == kOutMma) {
         // ============================================================ scores, Q S and P V
         const uint64_t dK = sw128_desc(0, 16, 1024);          // K-major
