@@ -555,23 +555,6 @@ def decode_tokens(q, k, v, log_g, beta, S, *, o=None, stream=None):
     return o
 
 
-class _Current:
-    """Stands for ``torch.cuda.device(device)`` where that device is the current one already."""
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        return False
-
-
-_CURRENT = _Current()
-
-
-def _device(device):
-    return _CURRENT if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
-
-
 def _handle(stream, device):
     """Raw handle of `stream`, or of the device's current stream."""
     if stream is None:
@@ -583,20 +566,28 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream):
-    """Allocate for work on `stream`: a tensor made here comes from that stream's memory, so that
-    nothing pending on the current stream still uses it and its reuse follows the call."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(like, shape, dtype, stream):
+    """An uninitialised tensor for work on `stream`, from that stream's memory, so that nothing
+    pending on the current stream still uses it and its reuse follows the call."""
+    if stream is None:
+        return (torch.empty_like(like) if shape is None
+                else torch.empty(shape, dtype=dtype, device=like.device))
+    with torch.cuda.stream(stream):
+        return _empty(like, shape, dtype, None)
+
+
+def _call(fn, where, device, *args):
+    """Call the library with `device` current, and check the status."""
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != 0:
+        _check(st, where)
 
 
 GATE_TOKEN, GATE_HEAD = 0, 1
-
-
-def _linear_gate(log_g, shape, device):
-    """Gate kind of log_g: [H] (one decay for each head) or one per token and head."""
-    one = isinstance(log_g, torch.Tensor) and log_g.dim() == 1
-    _dev(log_g, "log_g", torch.float32, shape[-1:] if one else shape, device)
-    return GATE_HEAD if one else GATE_TOKEN
 
 
 def linear_fwd_workspace_size(B, T, H, Hk, dk, dv, num_seqs, dtype=torch.bfloat16,
@@ -604,6 +595,26 @@ def linear_fwd_workspace_size(B, T, H, Hk, dk, dv, num_seqs, dtype=torch.bfloat1
     d = LinearDesc(B, T, H, Hk, dk, dv, num_seqs,
                    KDA_BF16 if dtype == torch.bfloat16 else KDA_F32, gate)
     return int(lib().kda_linear_fwd_workspace_size(ctypes.byref(d)))
+
+
+def _linear_inputs(q, k, v, log_g, lead_dims):
+    """Checks of linear attention's inputs: (device, q's shape, H, dv, gate kind). log_g is [H], one
+    decay for each head, or one per token and head."""
+    _dev(q, "q")
+    dev, qs = q.device, q.shape
+    if len(qs) not in lead_dims:
+        raise ValueError("q must be [B, T, Hk, dk] (or [N, Hk, dk] for one token)")
+    dt = q.dtype
+    _dev(k, "k", dt, qs, dev)
+    _dev(v, "v", dt, None, dev)
+    vs = v.shape
+    if len(vs) != len(qs) or vs[:-2] != qs[:-2]:
+        raise ValueError("v must be shaped like q but for its heads and head dim")
+    if not isinstance(log_g, torch.Tensor) or log_g.dim() != 1:
+        _dev(log_g, "log_g", torch.float32, vs[:-1], dev)
+        return dev, qs, vs[-2], vs[-1], GATE_TOKEN
+    _dev(log_g, "log_g", torch.float32, vs[-2:-1], dev)
+    return dev, qs, vs[-2], vs[-1], GATE_HEAD
 
 
 def linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, *, output_final_state: bool = True,
@@ -618,53 +629,37 @@ def linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, *, output_final_state: 
     overlap h0, nor o any input. The workspace (uint8, linear_fwd_workspace_size bytes) is
     allocated here when not given; calls that may overlap need one each.
     """
-    lib()
-    _dev(q, "q")
-    dev = q.device
-    if q.dim() != 4:
-        raise ValueError("q must be [B, T, Hk, dk]")
-    B, T, Hk, dk = q.shape
-    dt = q.dtype
-    _dtype_code(q)
-    _dev(k, "k", dt, (B, T, Hk, dk), dev)
-    _dev(v, "v", dt, None, dev)
-    if v.dim() != 4 or tuple(v.shape[:2]) != (B, T):
-        raise ValueError("v must be [B, T, H, dv]")
-    H, dv = v.shape[2:]
-    gate = _linear_gate(log_g, (B, T, H), dev)
+    L = lib()
+    dev, (B, T, Hk, dk), H, dv, gate = _linear_inputs(q, k, v, log_g, (4,))
     N = B
     if cu_seqlens is not None:
         _dev(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be a 1-D int32 tensor of N + 1 offsets")
         N = cu_seqlens.numel() - 1
-    _dev(h0, "h0", torch.float32, (N, H, dk, dv), dev)
+    state = (N, H, dk, dv)
+    _dev(h0, "h0", torch.float32, state, dev)
     if o is None:
-        with _on(stream):
-            o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        o = _empty(v, None, None, stream)
     else:
-        _dev(o, "o", dt, (B, T, H, dv), dev)
+        _dev(o, "o", q.dtype, v.shape, dev)
     if not output_final_state:
         hT = None
     elif hT is None:
-        with _on(stream):
-            hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        hT = _empty(v, state, torch.float32, stream)
     else:
-        _dev(hT, "hT", torch.float32, (N, H, dk, dv), dev)
-    desc = LinearDesc(B, T, H, Hk, dk, dv, N, _dtype_code(q), gate)
+        _dev(hT, "hT", torch.float32, state, dev)
+    desc = ctypes.byref(LinearDesc(B, T, H, Hk, dk, dv, N, _dtype_code(q), gate))
     if workspace is None:
-        need = int(lib().kda_linear_fwd_workspace_size(ctypes.byref(desc)))
-        if need > 0:
-            with _on(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = L.kda_linear_fwd_workspace_size(desc)
+        if ws_bytes > 0:
+            workspace = _empty(v, ws_bytes, torch.uint8, stream)
     else:
         _dev(workspace, "workspace", torch.uint8, None, dev)
-    ws_bytes = 0 if workspace is None else workspace.numel()
-    with _device(dev):
-        st = lib().kda_linear_fwd(ctypes.byref(desc), _at(q), _at(k), _at(v), _at(log_g),
-                                  _at(h0), _at(cu_seqlens), _at(o), _at(hT), _at(workspace),
-                                  ws_bytes, _handle(stream, dev))
-    _check(st, "kda_linear_fwd")
+        ws_bytes = workspace.numel()
+    _call(L.kda_linear_fwd, "kda_linear_fwd", dev, desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_g.data_ptr(), _at(h0), _at(cu_seqlens), o.data_ptr(), _at(hT), _at(workspace),
+          ws_bytes, _handle(stream, dev))
     return o, hT
 
 
@@ -672,32 +667,17 @@ def linear_decode(q, k, v, log_g, S, *, o=None, stream=None):
     """One token (q, k: [N, Hk, dk], v: [N, H, dv]) or T tokens ([N, T, ...]) of linear attention
     for N sequences (``kda_linear_decode``); S [N, H, dk, dv] fp32 is updated in place. log_g: fp32
     [N, H] or [N, T, H] to match, or [H] for one decay per head. Returns o like v."""
-    lib()
-    _dev(q, "q")
-    dev = q.device
-    if q.dim() not in (3, 4):
-        raise ValueError("q must be [N, Hk, dk] or [N, T, Hk, dk]")
-    lead = tuple(q.shape[:-2])
-    N, T = lead[0], lead[1] if len(lead) == 2 else 1
-    Hk, dk = q.shape[-2:]
-    dt = q.dtype
-    _dtype_code(q)
-    _dev(k, "k", dt, tuple(q.shape), dev)
-    _dev(v, "v", dt, None, dev)
-    if v.dim() != q.dim() or tuple(v.shape[:-2]) != lead:
-        raise ValueError("v must be %s" % ("[N, H, dv]" if len(lead) == 1 else "[N, T, H, dv]"))
-    H, dv = v.shape[-2:]
-    gate = _linear_gate(log_g, (*lead, H), dev)
+    L = lib()
+    dev, qs, H, dv, gate = _linear_inputs(q, k, v, log_g, (3, 4))
+    N, T, Hk, dk = qs if len(qs) == 4 else (qs[0], 1, qs[1], qs[2])
     _dev(S, "S", torch.float32, (N, H, dk, dv), dev)
     if o is None:
-        with _on(stream):
-            o = torch.empty(tuple(v.shape), dtype=dt, device=dev)
+        o = _empty(v, None, None, stream)
     else:
-        _dev(o, "o", dt, tuple(v.shape), dev)
-    with _device(dev):
-        st = lib().kda_linear_decode(N, T, H, Hk, dk, dv, _dtype_code(q), gate, _at(q), _at(k),
-                                     _at(v), _at(log_g), _at(S), _at(o), _handle(stream, dev))
-    _check(st, "kda_linear_decode")
+        _dev(o, "o", q.dtype, v.shape, dev)
+    _call(L.kda_linear_decode, "kda_linear_decode", dev, N, T, H, Hk, dk, dv, _dtype_code(q), gate,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), log_g.data_ptr(), S.data_ptr(), o.data_ptr(),
+          _handle(stream, dev))
     return o
 
 
@@ -712,9 +692,9 @@ def _tree_rows(k, v, log_g, beta, S):
         raise ValueError("k must be [N, T, H, 128]")
     N, T, H, d = k.shape
     _dtype_code(k)
-    _dev(v, "v", dt, (N, T, H, d), dev)
-    _dev(log_g, "log_g", torch.float32, (N, T, H, d), dev)
-    _dev(beta, "beta", dt, (N, T, H), dev)
+    _dev(v, "v", dt, k.shape, dev)
+    _dev(log_g, "log_g", torch.float32, k.shape, dev)
+    _dev(beta, "beta", dt, k.shape[:3], dev)
     _dev(S, "S", torch.float32, (N, H, d, d), dev)
     return dev, dt, N, T, H
 
@@ -730,34 +710,31 @@ def decode_tree(q, k, v, log_g, beta, parents, S, *, o=None, stream=None):
     """
     lib()
     dev, dt, N, T, H = _tree_rows(k, v, log_g, beta, S)
-    _dev(q, "q", dt, tuple(k.shape), dev)
+    _dev(q, "q", dt, k.shape, dev)
     _dev(parents, "parents", torch.int32, (N, T), dev)
     if o is None:
-        with _on(stream):
-            o = torch.zeros(tuple(k.shape), dtype=dt, device=dev)
+        o = _empty(k, None, None, stream)
+        with torch.cuda.stream(stream):   # (None: the current one)
+            o.zero_()
     else:
-        _dev(o, "o", dt, tuple(k.shape), dev)
-    with _device(dev):
-        st = lib().kda_decode_tree(N, H, T, _dtype_code(k), _at(q), _at(k), _at(v),
-                                   _at(log_g), _at(beta), _at(parents), _at(S), _at(o),
-                                   _handle(stream, dev))
-    _check(st, "kda_decode_tree")
+        _dev(o, "o", dt, k.shape, dev)
+    _call(lib().kda_decode_tree, "kda_decode_tree", dev, N, H, T, _dtype_code(k), q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), log_g.data_ptr(), beta.data_ptr(), parents.data_ptr(),
+          S.data_ptr(), o.data_ptr(), _handle(stream, dev))
     return o
 
 
 def commit_path(k, v, log_g, beta, path, S, *, stream=None):
     """Advance the states S in place by the rows that path names (``kda_commit_path``): int32
     [N, A], each row list ending at its first negative entry. Rows as for ``decode_tree``."""
-    lib()
+    L = lib()
     dev, dt, N, T, H = _tree_rows(k, v, log_g, beta, S)
     _dev(path, "path", torch.int32, None, dev)
     if path.dim() != 2 or path.shape[0] != N:
         raise ValueError("path must be [N, A]")
-    with _device(dev):
-        st = lib().kda_commit_path(N, H, T, path.shape[1], _dtype_code(k), _at(k), _at(v),
-                                   _at(log_g), _at(beta), _at(path), _at(S),
-                                   _handle(stream, dev))
-    _check(st, "kda_commit_path")
+    _call(L.kda_commit_path, "kda_commit_path", dev, N, H, T, path.shape[1], _dtype_code(k),
+          k.data_ptr(), v.data_ptr(), log_g.data_ptr(), beta.data_ptr(), path.data_ptr(),
+          S.data_ptr(), _handle(stream, dev))
 
 
 def state_copy(S, src, dst, *, page_dim: int = 0, stream=None):
@@ -766,25 +743,23 @@ def state_copy(S, src, dst, *, page_dim: int = 0, stream=None):
     where src[i] is -1; dst[i] = -1 does nothing. src, dst: int32 [n] on the device. S: any dtype,
     contiguous, a page's bytes a multiple of 16. No page may be written twice, or both read and
     written: such pairs, and ones out of range, are left out and set KDA_ERR_BAD_INDEX."""
-    lib()
+    L = lib()
     _dev(S, "S")
-    dev = S.device
-    if not 0 <= page_dim < S.dim():
+    dev, shape = S.device, S.shape
+    if not 0 <= page_dim < len(shape):
         raise ValueError("page_dim must be a dimension of S")
     _dev(src, "src", torch.int32, None, dev)
     if src.dim() != 1:
         raise ValueError("src must be 1-D")
-    _dev(dst, "dst", torch.int32, tuple(src.shape), dev)
+    _dev(dst, "dst", torch.int32, src.shape, dev)
     layers = 1
-    for x in S.shape[:page_dim]:
+    for x in shape[:page_dim]:
         layers *= x
     page = S.element_size()
-    for x in S.shape[page_dim + 1:]:
+    for x in shape[page_dim + 1:]:
         page *= x
-    with _device(dev):
-        st = lib().kda_state_copy(_at(S), layers, S.shape[page_dim], page, _at(src), _at(dst),
-                                  src.numel(), _handle(stream, dev))
-    _check(st, "kda_state_copy")
+    _call(L.kda_state_copy, "kda_state_copy", dev, S.data_ptr(), layers, shape[page_dim], page,
+          src.data_ptr(), dst.data_ptr(), src.numel(), _handle(stream, dev))
 
 
 def plan_compaction(live):
