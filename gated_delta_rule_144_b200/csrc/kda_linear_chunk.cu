@@ -136,13 +136,6 @@ __device__ __forceinline__ void sub2(float& a, float& b, float c, float d) {
         "mov.b64 m, {%4, %4};\n\tfma.rn.f32x2 x, y, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(a), "+f"(b) : "f"(c), "f"(d), "f"(-1.f));
 }
-// One box into L2 only.
-__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(tmap)),
-                 "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
@@ -577,21 +570,13 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         values(kOut ? 0 : 1);
     } else if (warp == kLoadWarp) {
         // ============================================================ loader
-        // Loads of a chunk follow its stage's release, a chunk before their use; its tiles are
-        // fetched into L2 two chunks before that, so that they then take an L2 hit's time.
+        // Loads of a chunk follow its stage's release, a chunk before their use. (Fetching the tiles
+        // into L2 two chunks before that as well: 1.15 ms against 1.10 on the long-context case.)
         constexpr int kBoxes = kOut ? 4 : 2;   // k's two panels, then q's
         auto place = [&](int m) { return m < 2 ? ST_K + m * kPanel : ST_Q + (m - 2) * kPanel; };
 #pragma unroll 1
-        for (int c = -2; c < nchunks; ++c) {
+        for (int c = 0; c < nchunks; ++c) {
             const int s = c & 1;
-            if (c + 4 < nchunks && lane == 0) {
-                const int t = (int)(sl.begin + (long long)(c + 4) * kC);
-#pragma unroll 1
-                for (int m = 0; m < kBoxes; ++m)
-                    tma_prefetch_3d(m < 2 ? &maps.k : &maps.q, 64 * (m & 1), hk, t);
-                tma_prefetch_3d(&maps.v, j0, h, t);
-            }
-            if (c < 0) continue;
             if (args.debug_stall && !wait(b_tail, 0)) break;
             if (c >= 2 && !wait(b_qkfree + 8 * s, (c >> 1) - 1)) break;
             const int valid = rows_of(c);
@@ -701,7 +686,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             if (c >= 0) {
                 if (!wait(b_s, c)) break;
                 tc_fence_after();   // (its columns of O2 are free: P V of c - 1 went after their reader)
-#pragma unroll 4
+#pragma unroll
                 for (int s = 0; s < 8; ++s)
                     umma_f16_warp(tbase + TM_O2 + 64 * (c & 1),
                                   desc_at(dK, st + ST_Q + (s >> 2) * kPanel + (s & 3) * 32),
@@ -713,7 +698,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             if (c + 1 < nchunks) {
                 if (!wait(b_full + 8 * ((c + 1) & 1), (c + 1) >> 1)) break;
                 tc_fence_after();
-#pragma unroll 4
+#pragma unroll
                 for (int s = 0; s < 8; ++s)
                     umma_f16_warp(tbase + TM_P,
                                   desc_at(dK, sn + ST_Q + (s >> 2) * kPanel + (s & 3) * 32),
@@ -725,7 +710,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
             if (c > 0 && !wait(b_ofree, c - 1)) break;
             if (!wait(b_vfull + 8 * (c & 1), c >> 1)) break;
             tc_fence_after();
-#pragma unroll 4
+#pragma unroll
             for (int s = 0; s < 8; ++s)
                 umma_f16_ts_warp(tbase + TM_O1, tbase + TM_PB + 8 * s,
                                  desc_at(dM, st + ST_V + 2048 * s), id_o, s > 0);
