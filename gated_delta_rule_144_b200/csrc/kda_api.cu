@@ -793,14 +793,16 @@ static bool linear_chunked(const kda_linear_desc_t* d) {
     return kda::linear_chunk_takes(d->dtype == KDA_BF16, d->dk, d->dv);
 }
 
-// Tokens per segment of the per-token walk (0: whole sequences). The walk has one warp per 8 value
-// columns of a (segment, head); segments are cut so that about 4096 warps (7 per scheduler) share
-// the work, and are not worth their states below 64 tokens.
+// Tokens per segment of the per-token walk (0: whole sequences). The walk has one warp per 16 value
+// columns of a (segment, head) (8 above dk = 128); segments are cut so that about 2048 warps share
+// the work (3 per scheduler; more cost a longer first pass: they are not worth their states below
+// 64 tokens).
 static int linear_walk_segment(const kda_linear_desc_t* d) {
-    const int64_t groups = (int64_t)d->H * ((d->dv + 7) / 8);
-    const int64_t want = ((int64_t)d->B * d->T * groups / 4096 + 31) / 32 * 32;
+    const int nc = d->dk <= 128 ? 16 : 8;
+    const int64_t groups = (int64_t)d->H * ((d->dv + nc - 1) / nc);
+    const int64_t want = ((int64_t)d->B * d->T * groups / 2048 + 31) / 32 * 32;
     const int L = (int)std::max<int64_t>(64, want);
-    if (d->num_seqs * groups >= 4096) return 0;
+    if (d->num_seqs * groups >= 2048) return 0;
     return d->T > L ? L : 0;
 }
 

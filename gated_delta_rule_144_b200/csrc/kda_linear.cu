@@ -5,134 +5,219 @@
 //     S <- g S + k v^T,   o = S^T q,   g = exp(log_g),
 // everything in fp32. It serves fp32 inputs and the sizes the tensor-core kernel does not take.
 //
-// Work split. Column j of S meets only column j of v, so one warp owns kNC value columns of one
-// (segment, head), with the dk rows spread over the lanes (lane l holds rows l, l + 32, ...). Per
-// token a lane does 2 fp32 operations per state element and one for the read-out; the read-out's
-// sum over the rows halves its columns at each butterfly step (4 + 2 + 1 + 1 + 1 shuffles for 8
-// columns). Bound: fp32 issue.
+// Work split. Column j of S meets only column j of v, so one warp owns NC value columns of one
+// (segment, head), with the dk rows spread over the lanes (lane l holds rows l, l + 32, ...); four
+// warps form a block. The block stages kTokens tokens' rows in shared memory while it works on the
+// kTokens before them: a token's arithmetic is shorter than a load's time. The state pairs its
+// columns, so that one two-lane instruction works on both. The read-out's sum over the rows halves
+// its columns at each butterfly step (8 + 4 + 2 + 1 + 1 shuffles for 16 columns). A segment's own
+// contribution (no read-out) is taken from its last token back, with the product of the gates
+// behind as a running factor of k: one multiply-add per element instead of two. Bound: issue.
+// (With the next token's rows fetched into registers instead, a token took a load's time: one
+// prompt of 4096 tokens x 16 heads in fp32 782 us.)
 
 #include "kda_linear.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kNC = 8;             // value columns per warp
-constexpr int kWarpsPerBlock = 4;
+constexpr int kWarpsPerBlock = 4, kBlock = 32 * kWarpsPerBlock;
+constexpr int kTokens = 16;   // staged at once
 
-// Sum of x[i] over the warp's lanes; lane l returns the sum of column l / 4.
-__device__ __forceinline__ float reduce8(const float (&x)[kNC], int lane) {
-    float y[4], z[2], w;
-    const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float keep = b4 ? x[4 + i] : x[i], give = b4 ? x[i] : x[4 + i];
-        y[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float keep = b3 ? y[2 + i] : y[i], give = b3 ? y[i] : y[2 + i];
-        z[i] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
-    }
-    w = (b2 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, b2 ? z[0] : z[1], 4);
-    w += __shfl_xor_sync(0xffffffffu, w, 2);
-    w += __shfl_xor_sync(0xffffffffu, w, 1);
-    return w;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
-template <typename Tin, int RPL>
-__global__ void __launch_bounds__(kWarpsPerBlock * 32)
-linear_walk_kernel(const LinearParams p, const LinearPass pass, const int col_groups) {
+// Sum of x[i] over the warp's lanes; lane l returns the sum of column l / (32 / NC).
+template <int NC>
+__device__ __forceinline__ float reduce_columns(float (&x)[NC], int lane) {
+    int off = 16;
+#pragma unroll
+    for (int n = NC / 2; n > 0; n /= 2, off /= 2) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            x[i] = (up ? x[n + i] : x[i]) +
+                   __shfl_xor_sync(0xffffffffu, up ? x[i] : x[n + i], off);
+    }
+    float y = x[0];
+#pragma unroll
+    for (; off > 0; off /= 2) y += __shfl_xor_sync(0xffffffffu, y, off);
+    return y;
+}
+
+__device__ __forceinline__ float2 pair_at(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 pair_at(const __nv_bfloat16* p) {
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+
+template <typename Tin, int RPL, int NC>
+struct WalkSmem {
+    static constexpr int kRow = 32 * RPL, kCols = NC * kWarpsPerBlock;
+    Tin q[2][kTokens][kRow], k[2][kTokens][kRow], v[2][kTokens][kCols];
+    float g[2][kTokens];
+};
+
+template <typename Tin, int RPL, int NC, bool kStates>
+__global__ void __launch_bounds__(kBlock)
+linear_walk_kernel(const __grid_constant__ LinearParams p, const int col_groups) {
+    using Smem = WalkSmem<Tin, RPL, NC>;
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(raw);
     const Tin* __restrict__ q = static_cast<const Tin*>(p.q);
     const Tin* __restrict__ k = static_cast<const Tin*>(p.k);
     const Tin* __restrict__ v = static_cast<const Tin*>(p.v);
     Tin* __restrict__ o = static_cast<Tin*>(p.o);
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (int64_t)blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
-    if (warp >= (int64_t)p.slots * p.H * col_groups) return;
-    const int cg = (int)(warp % col_groups);
-    const int h = (int)(warp / col_groups % p.H);
-    const int g = (int)(warp / col_groups / p.H);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cg = blockIdx.x % col_groups;
+    const int h = blockIdx.x / col_groups % p.H, g = blockIdx.x / col_groups / p.H;
     LinearSlot sl;
     if (!linear_slot(p, g, &sl)) return;
-    const bool states = pass == LinearPass::kStates;
-    if (states && sl.last) return;
+    if (kStates && sl.last) return;
 
-    const int dk = p.dk, dv = p.dv, j0 = cg * kNC;
+    const int dk = p.dk, dv = p.dv;
+    const int b0 = cg * Smem::kCols, bcols = min(Smem::kCols, dv - b0);   // the block's columns
+    const int j0 = b0 + warp * NC, cols = max(0, min(NC, dv - j0));       // the warp's
     const int hk = h / (p.H / p.Hk);
     const size_t unit = (size_t)dk * dv;
     const float* init = nullptr;
-    if (!states)
+    if (!kStates)
         init = sl.seg > 0 ? p.seg_state + ((size_t)g * p.H + h) * unit
                           : (p.h0 ? p.h0 + ((size_t)sl.n * p.H + h) * unit : nullptr);
-    float S[RPL][kNC];
+    float2 S[RPL][NC / 2];
 #pragma unroll
     for (int r = 0; r < RPL; ++r) {
         const int c = lane + 32 * r;
+        const float* at = init + (size_t)c * dv + j0;
 #pragma unroll
-        for (int i = 0; i < kNC; ++i)
-            S[r][i] = (init && c < dk && j0 + i < dv) ? init[(size_t)c * dv + j0 + i] : 0.f;
+        for (int i = 0; i < NC / 2; ++i)
+            S[r][i] = make_float2(init && c < dk && 2 * i < cols ? at[2 * i] : 0.f,
+                                  init && c < dk && 2 * i + 1 < cols ? at[2 * i + 1] : 0.f);
     }
 
-    float kr[RPL], qr[RPL], vr[kNC], lg = 0.f;
-    auto fetch = [&](int64_t t, float* kk, float* qq, float* vv, float& ll) {
-        const int64_t qk = (t * p.Hk + hk) * (int64_t)dk;
-        const int64_t vo = (t * p.H + h) * (int64_t)dv;
-#pragma unroll
-        for (int r = 0; r < RPL; ++r) {
-            const int c = lane + 32 * r;
-            kk[r] = c < dk ? load_elem(k, qk + c) : 0.f;
-            qq[r] = c < dk && !states ? load_elem(q, qk + c) : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < kNC; ++i) vv[i] = (j0 + i < dv) ? load_elem(v, vo + j0 + i) : 0.f;
-        ll = p.log_g[p.gate_head ? h : t * p.H + h];
-    };
-    if (sl.begin < sl.end) fetch(sl.begin, kr, qr, vr, lg);
-    float total = 0.f;
-
-    for (int64_t t = sl.begin; t < sl.end; ++t) {
-        float kn[RPL], qn[RPL], vn[kNC], ln = 0.f;
-        if (t + 1 < sl.end) fetch(t + 1, kn, qn, vn, ln);
-        const float gt = expf(lg);
-        total += lg;
-        float acc[kNC];
-#pragma unroll
-        for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
-#pragma unroll
-        for (int r = 0; r < RPL; ++r)
-#pragma unroll
-            for (int i = 0; i < kNC; ++i) {
-                S[r][i] = fmaf(kr[r], vr[i], gt * S[r][i]);
-                acc[i] = fmaf(qr[r], S[r][i], acc[i]);
+    // rows of tokens [t0, t0 + m) into buffer b: in 16-byte pieces where every row starts and ends
+    // on one
+    const bool pieces = dk * sizeof(Tin) % 16 == 0 && dv * sizeof(Tin) % 16 == 0;
+    auto rows = [&](Tin* to, int ld, const Tin* from, int64_t stride, int width, int m) {
+        if (pieces) {
+            constexpr int kEl = 16 / sizeof(Tin);
+            const int per = width / kEl;
+            for (int i = tid; i < m * per; i += kBlock) {
+                const int t = i / per, e = (i - t * per) * kEl;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(to + t * ld + e)),
+                             "l"(from + t * stride + e)
+                             : "memory");
             }
-        if (!states) {
-            const float oi = reduce8(acc, lane);
-            const int j = j0 + (lane >> 2);
-            if ((lane & 3) == 0 && j < dv) store_elem(o, (t * p.H + h) * (int64_t)dv + j, oi);
+        } else {
+            for (int i = tid; i < m * width; i += kBlock) {
+                const int t = i / width, e = i - t * width;
+                to[t * ld + e] = from[t * stride + e];
+            }
         }
+    };
+    auto stage = [&](int b, int64_t t0, int m) {
+        rows(sm.k[b][0], Smem::kRow, k + (t0 * p.Hk + hk) * dk, (int64_t)p.Hk * dk, dk, m);
+        if (!kStates)
+            rows(sm.q[b][0], Smem::kRow, q + (t0 * p.Hk + hk) * dk, (int64_t)p.Hk * dk, dk, m);
+        rows(sm.v[b][0], Smem::kCols, v + (t0 * p.H + h) * dv + b0, (int64_t)p.H * dv, bcols, m);
+        if (tid < m) sm.g[b][tid] = expf(p.log_g[p.gate_head ? h : (t0 + tid) * p.H + h]);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    // blocks of tokens in order, or (kStates) from the last back
+    const int64_t n = sl.end - sl.begin;
+    const int nblocks = (int)((n + kTokens - 1) / kTokens);
+    auto first = [&](int i) {
+        return sl.begin + (int64_t)(kStates ? nblocks - 1 - i : i) * kTokens;
+    };
+    auto count = [&](int i) { return (int)min((long long)kTokens, (long long)(sl.end - first(i))); };
+    if (nblocks > 0) stage(0, first(0), count(0));
+    float behind = 1.f;   // kStates: the product of the gates behind the token
+
+#pragma unroll 1
+    for (int i = 0; i < nblocks; ++i) {
+        const int b = i & 1, m = count(i);
+        const int64_t t0 = first(i);
+        if (i + 1 < nblocks) stage(b ^ 1, first(i + 1), count(i + 1));
+        if (i + 1 < nblocks) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+#pragma unroll 1
+        for (int x = 0; x < m; ++x) {
+            const int t = kStates ? m - 1 - x : x;
+            const float gt = sm.g[b][t];
+            float2 vr[NC / 2];
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
-            kr[r] = kn[r];
-            qr[r] = qn[r];
+            for (int e = 0; e < NC / 2; ++e) vr[e] = pair_at(&sm.v[b][t][warp * NC + 2 * e]);
+            if (kStates) {
+#pragma unroll
+                for (int r = 0; r < RPL; ++r) {
+                    const float kb = behind * load_elem(sm.k[b][t], lane + 32 * r);
+                    const float2 k2 = make_float2(kb, kb);
+#pragma unroll
+                    for (int e = 0; e < NC / 2; ++e) S[r][e] = fma2(k2, vr[e], S[r][e]);
+                }
+                behind *= gt;
+                continue;
+            }
+            const float2 g2 = make_float2(gt, gt);
+            float2 acc[NC / 2];
+#pragma unroll
+            for (int e = 0; e < NC / 2; ++e) acc[e] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < RPL; ++r) {   // rows behind dk: k and q hold no such column
+                const int c = lane + 32 * r;
+                const float kr = c < dk ? load_elem(sm.k[b][t], c) : 0.f;
+                const float qr = c < dk ? load_elem(sm.q[b][t], c) : 0.f;
+                const float2 k2 = make_float2(kr, kr), q2 = make_float2(qr, qr);
+#pragma unroll
+                for (int e = 0; e < NC / 2; ++e) {
+                    S[r][e] = fma2(k2, vr[e], mul2(g2, S[r][e]));
+                    acc[e] = fma2(q2, S[r][e], acc[e]);
+                }
+            }
+            float y[NC];
+#pragma unroll
+            for (int e = 0; e < NC / 2; ++e) y[2 * e] = acc[e].x, y[2 * e + 1] = acc[e].y;
+            const float sum = reduce_columns<NC>(y, lane);
+            constexpr int kLanes = 32 / NC;   // per column
+            const int j = lane / kLanes;
+            if (lane % kLanes == 0 && j < cols)
+                store_elem(o, ((t0 + t) * p.H + h) * (int64_t)dv + j0 + j, sum);
         }
-#pragma unroll
-        for (int i = 0; i < kNC; ++i) vr[i] = vn[i];
-        lg = ln;
+        __syncthreads();
     }
 
-    float* out = states ? p.seg_state + ((size_t)g * p.H + h) * unit
-                        : (sl.last && p.hT ? p.hT + ((size_t)sl.n * p.H + h) * unit : nullptr);
+    float* out = kStates ? p.seg_state + ((size_t)g * p.H + h) * unit
+                         : (sl.last && p.hT ? p.hT + ((size_t)sl.n * p.H + h) * unit : nullptr);
     if (out) {
 #pragma unroll
         for (int r = 0; r < RPL; ++r) {
             const int c = lane + 32 * r;
             if (c >= dk) continue;
+            float* to = out + (size_t)c * dv + j0;
 #pragma unroll
-            for (int i = 0; i < kNC; ++i)
-                if (j0 + i < dv) out[(size_t)c * dv + j0 + i] = S[r][i];
+            for (int i = 0; i < NC / 2; ++i) {
+                if (2 * i < cols) to[2 * i] = S[r][i].x;
+                if (2 * i + 1 < cols) to[2 * i + 1] = S[r][i].y;
+            }
         }
     }
-    if (states && cg == 0 && lane == 0) p.seg_decay[(size_t)g * p.H + h] = expf(total);
+    if (kStates && cg == 0 && tid == 0) p.seg_decay[(size_t)g * p.H + h] = behind;
 }
 
 // The state before segment s of a sequence is d_{s-1} (state before s - 1) + B_{s-1}; the B of a
@@ -187,24 +272,40 @@ __global__ void linear_check_kernel(const int32_t* __restrict__ cu, int N, int T
         set_device_error(err, DEV_BAD_SEQLENS);
 }
 
-template <typename Tin, int RPL>
-cudaError_t launch_walk_typed(const LinearParams& p, LinearPass pass, cudaStream_t stream) {
-    const int col_groups = (p.dv + kNC - 1) / kNC;
-    const int64_t warps = (int64_t)p.slots * p.H * col_groups;
-    const int64_t blocks = (warps + kWarpsPerBlock - 1) / kWarpsPerBlock;
+PerDevice g_walk_setup[2][4][2];   // by type, rows per lane and pass
+
+template <typename Tin, int RPL, int NC, bool kStates>
+cudaError_t launch_walk_typed(const LinearParams& p, PerDevice& setup, cudaStream_t stream) {
+    using Smem = WalkSmem<Tin, RPL, NC>;
+    const cudaError_t e = setup.run([](int) {
+        return cudaFuncSetAttribute(linear_walk_kernel<Tin, RPL, NC, kStates>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sizeof(Smem));
+    });
+    if (e != cudaSuccess) return e;
+    const int col_groups = (p.dv + Smem::kCols - 1) / Smem::kCols;
+    const int64_t blocks = (int64_t)p.slots * p.H * col_groups;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
-    linear_walk_kernel<Tin, RPL>
-        <<<(unsigned)blocks, kWarpsPerBlock * 32, 0, stream>>>(p, pass, col_groups);
+    linear_walk_kernel<Tin, RPL, NC, kStates>
+        <<<(unsigned)blocks, kBlock, sizeof(Smem), stream>>>(p, col_groups);
     return cudaGetLastError();
+}
+
+template <typename Tin, int RPL, int NC>
+cudaError_t launch_walk_pass(const LinearParams& p, LinearPass pass, int rows,
+                             cudaStream_t stream) {
+    PerDevice(&setup)[2] = g_walk_setup[p.bf16][rows];
+    return pass == LinearPass::kStates ? launch_walk_typed<Tin, RPL, NC, true>(p, setup[0], stream)
+                                       : launch_walk_typed<Tin, RPL, NC, false>(p, setup[1], stream);
 }
 
 template <typename Tin>
 cudaError_t launch_walk_rpl(const LinearParams& p, LinearPass pass, cudaStream_t stream) {
-    if (p.dk <= 32) return launch_walk_typed<Tin, 1>(p, pass, stream);
-    if (p.dk <= 64) return launch_walk_typed<Tin, 2>(p, pass, stream);
-    if (p.dk <= 128) return launch_walk_typed<Tin, 4>(p, pass, stream);
-    return launch_walk_typed<Tin, 8>(p, pass, stream);
+    if (p.dk <= 32) return launch_walk_pass<Tin, 1, 16>(p, pass, 0, stream);
+    if (p.dk <= 64) return launch_walk_pass<Tin, 2, 16>(p, pass, 1, stream);
+    if (p.dk <= 128) return launch_walk_pass<Tin, 4, 16>(p, pass, 2, stream);
+    return launch_walk_pass<Tin, 8, 8>(p, pass, 3, stream);   // (the same registers of state)
 }
 
 }  // namespace
