@@ -136,9 +136,6 @@ __device__ __forceinline__ void sub2(float& a, float& b, float c, float d) {
         "mov.b64 m, {%4, %4};\n\tfma.rn.f32x2 x, y, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(a), "+f"(b) : "f"(c), "f"(d), "f"(-1.f));
 }
-__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -149,12 +146,15 @@ struct ChunkSlot {
     long long begin, end;
     bool last;
 };
-constexpr int kSorted = 1024;   // packed slots up to which CTAs take them longest first
+constexpr int kSorted = 128;    // packed slots up to which CTAs take them longest first (a CTA ranks
+                                // all of them: 32 comparisons per thread)
+constexpr int kScanned = 1024;  // packed sequences up to which every CTA reads all offsets
 
 // The CTA's g-th slot, found by the whole block; `tmp` is kSorted ints of shared memory. Equal
 // lengths: first segments first (they wait for nothing). Packed: longest first up to kSorted
-// slots, so that no long one starts last; every CTA reads all offsets, and a malformed cu_seqlens
-// makes each of them report it and stop. False: nothing to do.
+// slots, so that no long one starts last. Every CTA reads all offsets, and a malformed cu_seqlens
+// makes each of them report it and stop; above kScanned sequences, which are never cut into
+// segments, each checks its own, and some CTA meets what is malformed. False: nothing to do.
 __device__ __forceinline__ bool chunk_slot(const LinearParams& p, int g, int tid, int* tmp,
                                            ChunkSlot* s) {
     const int L = p.seg_tokens;
@@ -171,6 +171,15 @@ __device__ __forceinline__ bool chunk_slot(const LinearParams& p, int g, int tid
     }
     const int32_t* __restrict__ cu = p.cu_seqlens;
     bool bad = false;
+    if (p.N > kScanned) {
+        const int c0 = cu[g], c1 = cu[g + 1];
+        if (c0 < 0 || c1 < c0 || c1 > p.T || (g == 0 && c0 != 0) || (g == p.N - 1 && c1 != p.T)) {
+            if (tid == 0) set_device_error(p.err, DEV_BAD_SEQLENS);
+            return false;
+        }
+        *s = ChunkSlot{g, 0, g, c0, c1, true};
+        return true;
+    }
     for (int i = tid; i <= p.N; i += kThreads) {
         const int c = cu[i];
         bad |= (i == 0 && c != 0) || (i == p.N && c != p.T) || (i < p.N && cu[i + 1] < c);
@@ -250,7 +259,8 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     // buffer)
     const uint32_t nb = sb + OFF_BAR;
     const uint32_t b_full = nb, b_qkfree = nb + 16, b_vfree = nb + 32, b_gfull = nb + 48,
-                   b_gfree = nb + 64, b_vh = nb + 208, b_vhfree = nb + 240, b_kv = nb + 80,
+                   b_gfree = nb + 64, b_vh = nb + 208, b_vhfree = nb + 240, b_outfree = nb + 112,
+                   b_out = nb + 192, b_kv = nb + 80,
                    b_kvfree = nb + 96, b_p = nb + 120, b_pb = nb + 128, b_s = nb + 136,
                    b_sfree = nb + 144, b_o = nb + 152, b_ofree = nb + 160, b_tail = nb + 168,
                    b_vfull = nb + 176;
@@ -277,6 +287,8 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         mbar_init(b_o, 1);
         mbar_init(b_ofree, 128);
         mbar_init(b_tail, 1);
+        mbar_init(b_outfree, 1);
+        mbar_init(b_out, 128);
         fence_mbar_init();
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
@@ -436,8 +448,11 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
             }
             if (c > 0) {   // o = P V + e^G (Q S) of chunk c - 1, staged in shared memory
-                if (tid == 0) bulk_wait_read_all();   // the previous output has left it
-                bar_sync(1, 128);
+                if (tid == 0) {
+                    bulk_wait_read_all();   // the previous output has left it
+                    mbar_arrive(b_outfree);
+                }
+                if (!wait(b_outfree, c - 1)) break;
                 uint8_t* to = sm + OFF_OUT + row * 128;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
@@ -463,10 +478,14 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 const long long t = sl.begin + (long long)(c - 1) * kC;
                 if (valid == kC) {
                     fence_proxy_async();
-                    bar_sync(1, 128);
-                    if (tid == 0) {
-                        tma_store_3d(&maps.o, sb + OFF_OUT, j0, h, (int)t);
-                        bulk_commit();
+                    mbar_arrive(b_out);
+                    if (warp == 0) {
+                        if (!wait(b_out, c - 1)) break;
+                        if (lane == 0) {
+                            tma_store_3d(&maps.o, sb + OFF_OUT, j0, h, (int)t);
+                            bulk_commit();
+                        }
+                        __syncwarp();
                     }
                 } else if (row < valid) {   // not the rows behind the sequence's end
                     __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.o) +

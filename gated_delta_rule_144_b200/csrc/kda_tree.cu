@@ -16,8 +16,8 @@
 //            gates.
 //   paths    d_i of every node in log2(depth) rounds that each double the stretch of path covered.
 //   pairs    d_ij = d_i / d_j, so all pairs are one product [k d; q d] (k / d)^T on the tensor
-//            cores, of which the tree keeps its own. Where some d is below 1e-30 (a gate of -inf
-//            included) the quotient is out of range: then a warp per node walks the node's
+//            cores, of which the tree keeps its own. Where some d is below 1e-20 (a gate of -inf
+//            included) the quotient leaves the range: then a warp per node walks the node's
 //            ancestors with d_ij in registers, where only products of gates <= 1 appear.
 //   product  [k d; q d] S on the tensor cores (warp-level tf32 products: 16 x 8 x 8). The tree of
 //            bf16 rows uses one tf32 product (its operands lose at most 2^-11 and 2^-10, below the
@@ -45,7 +45,8 @@ constexpr int tree_threads(int nb) { return nb > 2 ? 512 : 256; }
 constexpr int kB = 16;       // nodes per block of the solve
 constexpr int kLd = 136;     // floats per row of the products
 constexpr int kLk = 132;     // floats per row of k: eight rows' fragments in different banks
-constexpr float kSteep = 1e-30f;   // path products below this take the direct walk
+constexpr float kSteep = 1e-20f;   // a path product below this, or a quotient above the other,
+constexpr float kLarge = 1e30f;    // takes the direct walk
 constexpr uint32_t kStateBytes = kD * kD * 4;
 constexpr uint32_t kWaitCycles = 1u << 31;   // about one second
 
@@ -69,6 +70,14 @@ __device__ __forceinline__ uint32_t tf32_rn(float x) {
 
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"((uint32_t)pred), "r"(id), "r"(count) : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -333,23 +342,23 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     const float* path = s_d + at * kN * kD;
     const unsigned long long* s_above = sm.above[at];
     // the left operand's rows k d and q d; k / d for the pairs
+    float4 over[kMine];
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
-        const float4 d = load4(path + (m * kWarps + warp) * kD + 4 * lane);
-        steep |= !(fminf(fminf(d.x, d.y), fminf(d.z, d.w)) >= kSteep);
-        steep |= d.x != d.x || d.y != d.y || d.z != d.z || d.w != d.w;
-        kd[m] = mul4(kd[m], d);
+        const float4 d = load4(path + (m * kWarps + warp) * kD + 4 * lane), x = kd[m];
+        over[m] = make_float4(x.x / d.x, x.y / d.y, x.z / d.z, x.w / d.w);
+        kd[m] = mul4(x, d);
         qd[m] = mul4(qd[m], d);
+        auto size = [](float4 a) { return (fabsf(a.x) + fabsf(a.y)) + (fabsf(a.z) + fabsf(a.w)); };
+        steep |= !(fminf(d.x, d.y) >= kSteep && fminf(d.z, d.w) >= kSteep && size(d) <= 4.f);
+        // (a k that is infinite or NaN itself spoils its node's pairs only, either way)
+        steep |= size(x) <= kLarge && !(size(over[m]) <= kLarge);
     }
     steep = __syncthreads_or(steep);
     if (!steep) {
 #pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-            const int i = m * kWarps + warp;
-            float4* to = reinterpret_cast<float4*>(sm.k + i * kLk + 4 * lane);
-            const float4 x = *to, d = load4(path + i * kD + 4 * lane);
-            *to = make_float4(x.x / d.x, x.y / d.y, x.z / d.z, x.w / d.w);
-        }
+        for (int m = 0; m < kMine; ++m)
+            *reinterpret_cast<float4*>(sm.k + (m * kWarps + warp) * kLk + 4 * lane) = over[m];
         __syncthreads();
     } else {
         direct_pairs<Tin, NB>(sm, p, n, h, warp, lane);
@@ -617,7 +626,8 @@ commit_path_kernel(const TreeParams p, const int units) {
     for (int it = 0;; ++it) {
         const int b = it & 1;
         const bool ok = mbar_wait(full + 8 * b, (it >> 1) & 1, kWaitCycles);
-        if (!__all_sync(0xffffffffu, ok)) {
+        // all workers go on or none (also: everyone is done with the rows before these)
+        if (bar_or(1, kPathWorkers, !ok)) {
             if (lane == 0) set_device_error(p.err, DEV_TIMEOUT);
             return;
         }
@@ -658,7 +668,7 @@ commit_path_kernel(const TreeParams p, const int units) {
             // channel tid: products of gates up to each row, from behind each row, between rows
             const float p0 = gg[0], p1 = p0 * gg[1], p2 = p1 * gg[2], p3 = p2 * gg[3];
             const float q2 = gg[3], q1 = gg[2] * q2, q0 = gg[1] * q1;
-            bar_sync(1, kPathWorkers);   // everyone has read the rows before these
+            if (a0 > 0) bar_sync(1, kPathWorkers);   // everyone has read the rows before these
             sm.kd[tid] = make_float4(kk[0] * p0, kk[1] * p1, kk[2] * p2, kk[3] * p3);
             sm.ke[tid] = make_float4(kk[0] * q0, kk[1] * q1, kk[2] * q2, kk[3]);
             sm.end[tid] = p3;

@@ -6,6 +6,10 @@ products whose roundings (2^-24 each) stay below 1e-6 together. bf16 o: 5e-3; it
 scores and the state that a chunk reads, each as much again, on disjoint parts of the sum.
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -253,3 +257,26 @@ def test_packed_few_heads(lens):
     cu = cu_of(lens)
     o, hT = kda.linear_fwd(x["q"], x["k"], x["v"], x["log_g"], h0=x["h0"], cu_seqlens=cu)
     check(x, o, hT, cu)
+
+
+def test_expired_wait_reports_timeout_and_context_survives():
+    """Failure injection: with KDA_DEBUG_STALL_WAIT set, the loader of every chunked CTA waits
+    (bounded by a 2M-cycle budget) on a barrier that nothing signals, and every other role runs
+    into its own bound. The kernel must report KDA_ERR_TIMEOUT, free TMEM and return; the context
+    must stay usable. Runs in a child process: the hooks are read once per process."""
+    code = (
+        "import torch, gated_delta_rule_144_b200 as kda\n"
+        "mk = lambda dt: [torch.randn(1, 600, 2, 128, device='cuda').to(dt) for _ in range(3)]\n"
+        "g = -torch.rand(1, 600, 2, device='cuda')\n"
+        "kda.linear_fwd(*mk(torch.bfloat16), g)\n"
+        "st = kda.get_device_error()\n"
+        "kda.linear_fwd(*mk(torch.float32), g)\n"
+        "torch.cuda.synchronize()\n"
+        "print('STATUS', st, int(kda.get_device_error()))\n")
+    env = dict(os.environ, KDA_DEBUG_WAIT_CYCLES="2000000", KDA_DEBUG_STALL_WAIT="1")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], env=env, cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    line = [x for x in r.stdout.splitlines() if x.startswith("STATUS")][-1]
+    assert line.split()[1:] == ["4", "0"]
