@@ -91,6 +91,7 @@ linear_walk_kernel(const __grid_constant__ LinearParams p, const int col_groups)
     const int dk = p.dk, dv = p.dv;
     const int b0 = cg * Smem::kCols, bcols = min(Smem::kCols, dv - b0);   // the block's columns
     const int j0 = b0 + warp * NC, cols = max(0, min(NC, dv - j0));       // the warp's
+    const bool whole = cols == NC && dv % 4 == 0;   // (16-byte pieces of state rows)
     const int hk = h / (p.H / p.Hk);
     const size_t unit = (size_t)dk * dv;
     const float* init = nullptr;
@@ -102,6 +103,15 @@ linear_walk_kernel(const __grid_constant__ LinearParams p, const int col_groups)
     for (int r = 0; r < RPL; ++r) {
         const int c = lane + 32 * r;
         const float* at = init + (size_t)c * dv + j0;
+        if (whole && init && c < dk) {
+#pragma unroll
+            for (int i = 0; i < NC / 2; i += 2) {
+                const float4 x = *reinterpret_cast<const float4*>(at + 2 * i);
+                S[r][i] = make_float2(x.x, x.y);
+                S[r][i + 1] = make_float2(x.z, x.w);
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < NC / 2; ++i)
             S[r][i] = make_float2(init && c < dk && 2 * i < cols ? at[2 * i] : 0.f,
@@ -210,6 +220,13 @@ linear_walk_kernel(const __grid_constant__ LinearParams p, const int col_groups)
             const int c = lane + 32 * r;
             if (c >= dk) continue;
             float* to = out + (size_t)c * dv + j0;
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < NC / 2; i += 2)
+                    *reinterpret_cast<float4*>(to + 2 * i) =
+                        make_float4(S[r][i].x, S[r][i].y, S[r][i + 1].x, S[r][i + 1].y);
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) {
                 if (2 * i < cols) to[2 * i] = S[r][i].x;

@@ -136,6 +136,17 @@ __device__ __forceinline__ void sub2(float& a, float& b, float c, float d) {
         "mov.b64 m, {%4, %4};\n\tfma.rn.f32x2 x, y, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(a), "+f"(b) : "f"(c), "f"(d), "f"(-1.f));
 }
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"((uint32_t)pred), "r"(id), "r"(count) : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -259,8 +270,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     // buffer)
     const uint32_t nb = sb + OFF_BAR;
     const uint32_t b_full = nb, b_qkfree = nb + 16, b_vfree = nb + 32, b_gfull = nb + 48,
-                   b_gfree = nb + 64, b_vh = nb + 208, b_vhfree = nb + 240, b_outfree = nb + 112,
-                   b_out = nb + 192, b_kv = nb + 80,
+                   b_gfree = nb + 64, b_vh = nb + 208, b_vhfree = nb + 240, b_kv = nb + 80,
                    b_kvfree = nb + 96, b_p = nb + 120, b_pb = nb + 128, b_s = nb + 136,
                    b_sfree = nb + 144, b_o = nb + 152, b_ofree = nb + 160, b_tail = nb + 168,
                    b_vfull = nb + 176;
@@ -287,8 +297,6 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         mbar_init(b_o, 1);
         mbar_init(b_ofree, 128);
         mbar_init(b_tail, 1);
-        mbar_init(b_outfree, 1);
-        mbar_init(b_out, 128);
         fence_mbar_init();
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
@@ -382,18 +390,16 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         // chunk c's scores, then, while chunk c + 1's are multiplied, chunk c - 1's output
         const uint32_t pb = tbase + lq + TM_PB;
         float er_last = 0.f;
+        bool ok = true;
 #pragma unroll 1
         for (int c = 0; kOut && nchunks > 0 && c <= nchunks; ++c) {
             float er = 0.f;
-            if (c < nchunks) {
-                if (!wait(b_gfull + 8 * (c & 1), c >> 1)) break;
-                if (!wait(b_p, c)) break;
-            }
+            if (c < nchunks) ok = ok && wait(b_gfull + 8 * (c & 1), c >> 1) && wait(b_p, c);
             // P V of the chunk before is done: its bf16 scores' columns are free and its output
             // is there
-            if (c > 0 && !wait(b_o, c - 1)) break;
+            if (c > 0) ok = ok && wait(b_o, c - 1);
             tc_fence_after();
-            if (c < nchunks) {
+            if (ok && c < nchunks) {
                 const float* gt = gates(c);
                 const float loc = gt[row], pre = ex2(loc);
                 // the blocks before this row's: what the suffix of block b lacks to reach the row
@@ -448,11 +454,9 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 if (lane == 0) mbar_arrive(b_gfree + 8 * (c & 1));
             }
             if (c > 0) {   // o = P V + e^G (Q S) of chunk c - 1, staged in shared memory
-                if (tid == 0) {
-                    bulk_wait_read_all();   // the previous output has left it
-                    mbar_arrive(b_outfree);
-                }
-                if (!wait(b_outfree, c - 1)) break;
+                if (tid == 0) bulk_wait_read_all();   // the previous output has left it
+                // (the four warps go on together: one whose wait expired comes here too)
+                if (bar_or(1, 128, !ok)) break;
                 uint8_t* to = sm + OFF_OUT + row * 128;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
@@ -478,14 +482,10 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 const long long t = sl.begin + (long long)(c - 1) * kC;
                 if (valid == kC) {
                     fence_proxy_async();
-                    mbar_arrive(b_out);
-                    if (warp == 0) {
-                        if (!wait(b_out, c - 1)) break;
-                        if (lane == 0) {
-                            tma_store_3d(&maps.o, sb + OFF_OUT, j0, h, (int)t);
-                            bulk_commit();
-                        }
-                        __syncwarp();
+                    bar_sync(1, 128);
+                    if (tid == 0) {
+                        tma_store_3d(&maps.o, sb + OFF_OUT, j0, h, (int)t);
+                        bulk_commit();
                     }
                 } else if (row < valid) {   // not the rows behind the sequence's end
                     __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.o) +

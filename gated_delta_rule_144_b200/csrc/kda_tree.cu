@@ -48,7 +48,7 @@ constexpr int kLk = 132;     // floats per row of k: eight rows' fragments in di
 constexpr float kSteep = 1e-20f;   // a path product below this, or a quotient above the other,
 constexpr float kLarge = 1e30f;    // takes the direct walk
 constexpr uint32_t kStateBytes = kD * kD * 4;
-constexpr uint32_t kWaitCycles = 1u << 31;   // about one second
+constexpr long long kWaitCycles = 1ll << 31;   // about one second
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -70,14 +70,6 @@ __device__ __forceinline__ uint32_t tf32_rn(float x) {
 
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r) : "r"((uint32_t)pred), "r"(id), "r"(count) : "memory");
-    return r != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -533,12 +525,12 @@ template <typename Tin>
 struct PathSmem {
     float state[kD * kD];           // the next unit's state
     Tin k[2][kRows][kD], v[2][kRows][kD];   // first rows of this unit and the next
-    float g[2][kRows][kD];
+    float g[2][kRows][kD], beta[2][kRows];
     float4 kd[kD], ke[kD];          // [channel][row]: k_j d_j, d_ej k_j
     float end[kD];                  // d_e
     float pairs[4][8];              // per warp: pair sums
     int unit[2], len[2];            // (unit at the end of the walk: -1)
-    unsigned long long full[2], free;
+    unsigned long long full[2], ready[2], free;
 };
 
 template <typename Tin>
@@ -549,10 +541,13 @@ commit_path_kernel(const TreeParams p, const int units) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Tin* k = static_cast<const Tin*>(p.k);
     const Tin* v = static_cast<const Tin*>(p.v);
-    const uint32_t full = smem_u32(sm.full), free = smem_u32(&sm.free);
+    const uint32_t full = smem_u32(sm.full), ready = smem_u32(sm.ready),
+                   free = smem_u32(&sm.free);
     if (tid == 0) {
         mbar_init(full, 1);
         mbar_init(full + 8, 1);
+        mbar_init(ready, 1);
+        mbar_init(ready + 8, 1);
         mbar_init(free, kPathWorkers);
         fence_mbar_init();
     }
@@ -583,15 +578,22 @@ commit_path_kernel(const TreeParams p, const int units) {
             if (len == 0) continue;
             // the workers have the previous state in registers, and are done with this buffer's
             // rows
-            if (it > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(free, (it - 1) & 1, kWaitCycles));
-                if (!ok) break;
-            }
             const int b = it & 1, m = min(len, kRows);
+            if (it > 0) ok = __all_sync(0xffffffffu, mbar_wait(free, (it - 1) & 1, kWaitCycles));
+            if (!ok) {   // (nothing of this CTA is in flight)
+                if (lane == 0) {
+                    sm.unit[b] = -1;
+                    mbar_arrive(ready + 8 * b);
+                }
+                break;
+            }
             const uint32_t bar = full + 8 * b;
+            if (lane < kRows)
+                sm.beta[b][lane] = lane < m ? load_elem(static_cast<const Tin*>(p.beta),
+                                                        ((int64_t)n * p.T + first) * p.H + h)
+                                            : 0.f;
+            __syncwarp();
             if (lane == 0) {
-                sm.unit[b] = unit;
-                sm.len[b] = len;
                 mbar_arrive_expect_tx(bar, kStateBytes + m * kD * (2 * sizeof(Tin) + 4));
                 for (int i = 0; i < 4; ++i)
                     bulk_load(smem_u32(sm.state) + i * (kStateBytes / 4),
@@ -605,18 +607,26 @@ commit_path_kernel(const TreeParams p, const int units) {
                 bulk_load(smem_u32(sm.v[b][lane]), v + at, kD * sizeof(Tin), bar);
                 bulk_load(smem_u32(sm.g[b][lane]), p.log_g + at, kD * 4, bar);
             }
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, (it >> 1) & 1, kWaitCycles));
+            if (lane == 0) {
+                sm.unit[b] = ok ? unit : -1;
+                sm.len[b] = len;
+                mbar_arrive(ready + 8 * b);
+            }
             __syncwarp();
             ++it;
         }
-        if (!ok) {   // the copy in flight lands first
+        if (!ok) {
             if (lane == 0) set_device_error(p.err, DEV_TIMEOUT);
-            mbar_wait(full + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1, kWaitCycles);
             return;
         }
-        if (it > 0) ok = __all_sync(0xffffffffu, mbar_wait(free, (it - 1) & 1, kWaitCycles));
+        // (the buffer of two units ago: free once the unit before is in registers)
+        if (it > 0 && !__all_sync(0xffffffffu, mbar_wait(free, (it - 1) & 1, kWaitCycles)) &&
+            lane == 0)
+            set_device_error(p.err, DEV_TIMEOUT);
         if (lane == 0) {
             sm.unit[it & 1] = -1;
-            mbar_arrive_expect_tx(full + 8 * (it & 1), 0);
+            mbar_arrive(ready + 8 * (it & 1));
         }
         return;
     }
@@ -625,23 +635,19 @@ commit_path_kernel(const TreeParams p, const int units) {
     const int phase = lane >> 3, col = 32 * warp + 4 * (lane & 7);
     for (int it = 0;; ++it) {
         const int b = it & 1;
-        const bool ok = mbar_wait(full + 8 * b, (it >> 1) & 1, kWaitCycles);
-        // all workers go on or none (also: everyone is done with the rows before these)
-        if (bar_or(1, kPathWorkers, !ok)) {
-            if (lane == 0) set_device_error(p.err, DEV_TIMEOUT);
-            return;
-        }
+        // one warp waits for all, so that they go on together or not at all (and all are done with
+        // the rows before these); the others' own look at the barrier orders the copies before
+        // their reads
+        // the loader arrives within two of its own bounds, whether the copies landed or not, so
+        // that the four warps always take the same way here (the look at `full` orders the copies
+        // before this thread's reads)
+        if (!mbar_wait(ready + 8 * b, (it >> 1) & 1, 8 * kWaitCycles)) return;
+        mbar_try_wait(full + 8 * b, (it >> 1) & 1);
         const int unit = sm.unit[b], len = sm.len[b];
         if (unit < 0) return;
         const int n = unit / p.H, h = unit % p.H;
         const int32_t* path = p.nodes + (size_t)n * p.A;
         auto row = [&](int a) { return (((size_t)n * p.T + path[a]) * p.H + h) * kD; };
-        float beta[kRows];   // of the first rows
-#pragma unroll
-        for (int j = 0; j < kRows; ++j)
-            beta[j] = j < len ? load_elem(static_cast<const Tin*>(p.beta),
-                                          ((int64_t)n * p.T + path[j]) * p.H + h)
-                              : 0.f;
         float4 s[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) s[i] = load4(sm.state + (phase + 4 * i) * kD + col);
@@ -661,14 +667,12 @@ commit_path_kernel(const TreeParams p, const int units) {
                     const size_t at = row(a0 + j) + tid;
                     kk[j] = load_elem(k, at);
                     gg[j] = expf(p.log_g[at]);
-                    beta[j] = load_elem(static_cast<const Tin*>(p.beta),
-                                        ((int64_t)n * p.T + path[a0 + j]) * p.H + h);
                 }
             }
             // channel tid: products of gates up to each row, from behind each row, between rows
             const float p0 = gg[0], p1 = p0 * gg[1], p2 = p1 * gg[2], p3 = p2 * gg[3];
             const float q2 = gg[3], q1 = gg[2] * q2, q0 = gg[1] * q1;
-            if (a0 > 0) bar_sync(1, kPathWorkers);   // everyone has read the rows before these
+            bar_sync(1, kPathWorkers);   // everyone has read the rows before these
             sm.kd[tid] = make_float4(kk[0] * p0, kk[1] * p1, kk[2] * p2, kk[3] * p3);
             sm.ke[tid] = make_float4(kk[0] * q0, kk[1] * q1, kk[2] * q2, kk[3]);
             sm.end[tid] = p3;
@@ -717,8 +721,11 @@ commit_path_kernel(const TreeParams p, const int units) {
                     r.x = fmaf(a, y[l].x, r.x), r.y = fmaf(a, y[l].y, r.y);
                     r.z = fmaf(a, y[l].z, r.z), r.w = fmaf(a, y[l].w, r.w);
                 }
-                y[j] = make_float4(beta[j] * r.x, beta[j] * r.y, beta[j] * r.z, beta[j] * r.w);
-                beta[j] = 0.f;   // (rows behind the path's end)
+                const float beta =
+                    a0 == 0 ? sm.beta[b][j]
+                    : a0 + j < len ? load_elem(static_cast<const Tin*>(p.beta), row(a0 + j) / kD)
+                                   : 0.f;
+                y[j] = make_float4(beta * r.x, beta * r.y, beta * r.z, beta * r.w);
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
