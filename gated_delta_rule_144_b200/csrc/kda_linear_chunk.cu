@@ -246,6 +246,94 @@ __device__ __forceinline__ bool chunk_slot(const LinearParams& p, int g, int tid
     return true;
 }
 
+// Row `row` of the state before the CTA's segment, N columns from `col`: h0, and on top of it the
+// states of the segments before, or their sum from a launch of its own (seg_ready).
+template <int N>
+__device__ __forceinline__ void initial_state(const LinearParams& p, const ChunkSlot& sl, int h,
+                                              int row, int col, float (&S)[N]) {
+    const size_t unit = (size_t)p.dk * p.dv, at = (size_t)row * p.dv + col;
+    auto add = [&](const float* from, float f) {   // S <- f S + what is at `from`
+        if (row >= p.dk) return;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            if (col + i >= p.dv) continue;
+            const float4 x = *reinterpret_cast<const float4*>(from + at + i);
+            S[i] = fmaf(f, S[i], x.x), S[i + 1] = fmaf(f, S[i + 1], x.y);
+            S[i + 2] = fmaf(f, S[i + 2], x.z), S[i + 3] = fmaf(f, S[i + 3], x.w);
+        }
+    };
+    const bool ready = p.seg_ready && sl.seg > 0;
+    if (sl.seg > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll 1
+    for (int i = ready ? 0 : sl.seg; i >= 0; --i) {
+        const size_t from = (size_t)(sl.slot - i) * p.H + h;
+        const bool start = i == sl.seg && !ready;
+        if (start && !p.h0) continue;
+        add(start ? p.h0 + ((size_t)sl.n * p.H + h) * unit
+                  : p.seg_state + (ready ? from : from - p.H) * unit,
+            start || ready ? 0.f : p.seg_decay[from - p.H]);
+    }
+}
+
+// In P V a value that is not finite also meets the zero scores of the rows before its own, and
+// 0 x NaN is NaN. The block computes the outputs of those rows (the rest of the chunk before the
+// first such value of a column) again, walking the segment token by token from its initial state.
+// Thread (row, group) holds 16 columns of a state row; `sm`: 64 + 4 * 64 words.
+__device__ __forceinline__ void repair_rows(const LinearParams& p, const ChunkSlot& sl, int h,
+                                            int j0, int tid, void* sm) {
+    int* first = static_cast<int*>(sm);                      // by column: its first such token
+    float(*sums)[kNV] = reinterpret_cast<float(*)[kNV]>(first + kNV);   // by warp of a group
+    const int len = (int)(sl.end - sl.begin), cols = min(kNV, p.dv - j0);
+    const long long vs = (long long)p.H * p.dv, ks = (long long)p.Hk * p.dk;
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + sl.begin * vs +
+                             (long long)h * p.dv + j0;
+    const long long k0 = sl.begin * ks + (long long)(h / (p.H / p.Hk)) * p.dk;
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + k0;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + k0;
+    if (tid < kNV) first[tid] = len;
+    __syncthreads();
+    if (tid % kNV < cols)
+#pragma unroll 1
+        for (int t = tid / kNV; t < len; t += kThreads / kNV)
+            if (!isfinite(__bfloat162float(v[t * vs + tid % kNV]))) {
+                atomicMin(first + tid % kNV, t);
+                break;
+            }
+    __syncthreads();
+    int end = 0;   // tokens to walk
+    for (int i = 0; i < cols; ++i)
+        if (first[i] < len && first[i] % kC) end = max(end, first[i]);
+    const int row = tid % kC, col = tid / kC * 16, lane = tid & 31;
+    float S[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[i] = 0.f;
+    if (end > 0) initial_state(p, sl, h, row, j0 + col, S);
+#pragma unroll 1
+    for (int t = 0; t < end; ++t) {
+        const float g = expf(p.log_g[p.gate_head ? h : (sl.begin + t) * p.H + h]);
+        const float kr = row < p.dk ? __bfloat162float(k[t * ks + row]) : 0.f;
+        const float qr = row < p.dk ? __bfloat162float(q[t * ks + row]) : 0.f;
+        bool any = false;   // whether a column's output is due
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            S[i] = fmaf(kr, col + i < cols ? __bfloat162float(v[t * vs + col + i]) : 0.f, g * S[i]);
+            any |= t < first[col + i] && t >= first[col + i] / kC * kC;
+        }
+        if (!__syncthreads_or(any)) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float x = qr * S[i];
+#pragma unroll
+            for (int off = 16; off > 0; off /= 2) x += __shfl_xor_sync(0xffffffffu, x, off);
+            if (lane == 0) sums[row / 32][col + i] = x;
+        }
+        __syncthreads();
+        if (tid < cols && t < first[tid] && t >= first[tid] / kC * kC && first[tid] < len)
+            static_cast<__nv_bfloat16*>(p.o)[((sl.begin + t) * p.H + h) * p.dv + j0 + tid] =
+                __float2bfloat16_rn((sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]));
+    }
+}
+
 // kOut: outputs (kWhole, kOutputs); else the states of segments (kStates).
 template <bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -316,6 +404,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
 
     // every lane waits; a warp goes on together or not at all
     bool failed = false;
+    bool spoilt = false;   // the state at the end is not finite
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
         const bool ok = __all_sync(0xffffffffu, wait_phase(bar, parity & 1u, args.budget));
         failed = !ok;
@@ -507,32 +596,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
         float S[kNV];
 #pragma unroll
         for (int i = 0; i < kNV; ++i) S[i] = 0.f;
-        // S <- f S + what is at `from`
-        auto add = [&](const float* from, float f) {
-            if (row >= p.dk) return;
-#pragma unroll
-            for (int i = 0; i < kNV; i += 4) {
-                if (j0 + i >= p.dv) continue;
-                const float4 x = *reinterpret_cast<const float4*>(from + at + i);
-                S[i] = fmaf(f, S[i], x.x), S[i + 1] = fmaf(f, S[i + 1], x.y);
-                S[i + 2] = fmaf(f, S[i + 2], x.z), S[i + 3] = fmaf(f, S[i + 3], x.w);
-            }
-        };
-        if (kOut) {
-            // h0; for a later segment the states of those before it on top of it, or, where they
-            // are many, their sum from a launch of its own (seg_ready)
-            const bool ready = p.seg_ready && sl.seg > 0;
-            if (sl.seg > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-#pragma unroll 1
-            for (int i = ready ? 0 : sl.seg; i >= 0; --i) {
-                const size_t from = (size_t)(sl.slot - i) * p.H + h;
-                const bool start = i == sl.seg && !ready;
-                if (start && !p.h0) continue;
-                add(start ? p.h0 + ((size_t)sl.n * p.H + h) * unit
-                          : p.seg_state + (ready ? from : from - p.H) * unit,
-                    start || ready ? 0.f : p.seg_decay[from - p.H]);
-            }
-        }
+        if (kOut) initial_state(p, sl, h, row, j0, S);
         auto publish = [&] {   // bf16 S, row `row`
             uint8_t* to = sm + OFF_SB + row * 128;
 #pragma unroll
@@ -574,6 +638,10 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
                 publish();
             }
         }
+        float zero = 0.f;
+#pragma unroll
+        for (int i = 0; kOut && i < kNV; ++i) zero = fmaf(0.f, S[i], zero);
+        spoilt = zero != 0.f && !failed;
         float* out = kOut ? (sl.last && p.hT ? p.hT + ((size_t)sl.n * p.H + h) * unit : nullptr)
                           : p.seg_state + ((size_t)sl.slot * p.H + h) * unit;
         if (out && !failed && row < p.dk) {
@@ -789,8 +857,13 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     // (this launch does not end before the one that it may have overtaken)
     if (kOut && warp == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
-    __syncthreads();
+    // (a value that is not finite leaves a state that is not, whatever follows it)
+    const bool again = __syncthreads_or(spoilt);
     if (warp == 0) tmem_dealloc(tbase, kTmemCols);
+    if (kOut && again) {
+        if (tid == 0) bulk_wait_all();   // the outputs' stores have landed
+        repair_rows(p, sl, h, j0, tid, sm);
+    }
 }
 
 uint32_t wait_budget() {

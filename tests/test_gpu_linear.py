@@ -136,6 +136,38 @@ def test_documents_do_not_leak(dtype, bad):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,spots", [   # (token, column); column None: the whole row
+    (300, [(200, 3)]), (300, [(128, None), (290, None)]), (300, [(255, None)]), (100, [(99, 0)]),
+    (700, [(600, 1), (300, 2), (690, 71), (0, 5)]), (9000, [(5003, 7), (8999, None)]),
+    (9000, [(1000, None)]),
+], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_bad_values_reach_no_earlier_token(T, spots, bad, dtype):
+    """An infinity or NaN in v spoils its column from its token on, and nothing else."""
+    x = make(1, T, 2, 1, 128, 72, dtype, seed=7)
+    ro, _ = linear_attention(*(host(x[n]) for n in ("q", "k", "v", "log_g", "h0")))
+    first = np.full(72, T)
+    for t, c in spots:
+        cols = slice(None) if c is None else c
+        x["v"][0, t, 1, cols] = bad
+        first[cols] = np.minimum(first[cols], t)
+    o, hT = kda.linear_fwd(**x)
+    assert kda.get_device_error() == 0
+    o, hT = host(o), host(hT)
+    clean = np.ones_like(o, dtype=bool)
+    clean[0, :, 1] = np.arange(T)[:, None] < first
+    assert rel_l2(o[clean], ro[clean]) <= (TOL_BF16 if dtype == "bf16" else TOL_F32)
+    for c in np.nonzero(first < T)[0]:   # the rows that are computed again, by themselves
+        rows = slice(first[c] // 128 * 128, first[c])
+        if rows.stop - rows.start > 8:
+            assert rel_l2(o[0, rows, 1, c], ro[0, rows, 1, c]) <= (
+                TOL_BF16 if dtype == "bf16" else TOL_F32)
+    assert not np.isfinite(o[~clean]).any()
+    assert np.isfinite(hT[0, 0]).all()
+    assert (np.isfinite(hT[0, 1]).all(0) == (first == T)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,T,H,Hk,dk,dv", [(1, 1, 1, 1, 128, 128), (5, 1, 4, 2, 128, 64),
                                             (3, 4, 2, 2, 128, 128), (2, 9, 3, 1, 64, 128),
                                             (2, 1, 2, 2, 32, 96), (1, 3, 1, 1, 256, 256),
