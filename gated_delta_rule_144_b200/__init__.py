@@ -19,7 +19,6 @@ Functions mirror the C entry points:
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from pathlib import Path
 
@@ -625,8 +624,8 @@ def linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, *, output_final_state: 
     q, k: [B, T, Hk, dk]; v: [B, T, H, dv], H a multiple of Hk (value head h reads q, k head
     h // (H / Hk)); q/k/v share one dtype (bf16 or fp32). log_g: fp32 [B, T, H], or [H] for one
     decay per head. h0: [N, H, dk, dv] fp32 or None. cu_seqlens: int32 [N + 1] on the device (B
-    must be 1) or None. Returns (o [B, T, H, dv], hT [N, H, dk, dv] fp32 or None). hT must not
-    overlap h0, nor o any input. The workspace (uint8, linear_fwd_workspace_size bytes) is
+    must be 1) or None. Returns (o [B, T, H, dv], hT [N, H, dk, dv] fp32 or None). o, hT and the
+    workspace must overlap nothing else. The workspace (uint8, linear_fwd_workspace_size bytes) is
     allocated here when not given; calls that may overlap need one each.
     """
     L = lib()

@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "kda.h"
@@ -759,7 +760,22 @@ kda_status_t kda_decode_tokens(int N, int H, int T, int dk, int dv, kda_dtype_t 
 
 static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + nb && y < x + na;
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+struct Span {
+    const void* at;
+    size_t bytes;
+    const char* name;
+};
+
+// No output overlaps an input or another output: the first `outputs` of `spans` are outputs.
+static kda_status_t check_apart(std::initializer_list<Span> spans, size_t outputs) {
+    for (const Span *a = spans.begin(); a < spans.begin() + outputs; ++a)
+        for (const Span* b = a + 1; b < spans.end(); ++b)
+            if (overlap(a->at, a->bytes, b->at, b->bytes))
+                return fail(KDA_ERR_INVALID_ARG, "%s overlaps %s", a->name, b->name);
+    return KDA_OK;
 }
 
 static kda_status_t check_linear_desc(const kda_linear_desc_t* d, bool has_cu) {
@@ -898,15 +914,19 @@ kda_status_t kda_linear_fwd(const kda_linear_desc_t* d, const void* q, const voi
     const size_t esz = d->dtype == KDA_BF16 ? 2 : 4, rows = (size_t)d->B * d->T;
     const size_t qk_bytes = rows * d->Hk * d->dk * esz, v_bytes = rows * d->H * d->dv * esz;
     const size_t h_bytes = (size_t)d->num_seqs * d->H * d->dk * d->dv * sizeof(float);
-    if (overlap(o, v_bytes, q, qk_bytes) || overlap(o, v_bytes, k, qk_bytes) ||
-        overlap(o, v_bytes, v, v_bytes))
-        return fail(KDA_ERR_INVALID_ARG, "o overlaps q, k or v");
-    if (overlap(hT, h_bytes, h0, h_bytes)) return fail(KDA_ERR_INVALID_ARG, "hT overlaps h0");
     const LinearLayout L = linear_layout(d, cu_seqlens != nullptr);
     if (L.total > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < L.total))
         return fail(KDA_ERR_INVALID_ARG,
                     "workspace must be a 16-byte aligned device buffer of %zu bytes "
                     "(kda_linear_fwd_workspace_size)", L.total);
+    const size_t gates = d->gate == KDA_GATE_HEAD ? d->H : rows * d->H;
+    if ((st = check_apart({{o, v_bytes, "o"}, {hT, h_bytes, "hT"},
+                          {L.total > 0 ? workspace : nullptr, L.total, "the workspace"},
+                          {q, qk_bytes, "q"}, {k, qk_bytes, "k"}, {v, v_bytes, "v"},
+                          {log_g, gates * 4, "log_g"}, {h0, h_bytes, "h0"},
+                          {cu_seqlens, ((size_t)d->num_seqs + 1) * 4, "cu_seqlens"}}, 3)) !=
+        KDA_OK)
+        return st;
     if (d->num_seqs == 0) return KDA_OK;
     kda::LinearParams p = linear_params(d);
     p.q = q; p.k = k; p.v = v; p.log_g = log_g; p.h0 = h0; p.cu_seqlens = cu_seqlens;
@@ -956,12 +976,11 @@ kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_
     const size_t esz = dtype == KDA_BF16 ? 2 : 4, rows = (size_t)N * T;
     const size_t qk_bytes = rows * Hk * dk * esz, v_bytes = rows * H * dv * esz;
     const size_t s_bytes = (size_t)N * H * dk * dv * sizeof(float);
-    if (overlap(o, v_bytes, q, qk_bytes) || overlap(o, v_bytes, k, qk_bytes) ||
-        overlap(o, v_bytes, v, v_bytes))
-        return fail(KDA_ERR_INVALID_ARG, "o overlaps q, k or v");
-    if (overlap(S_inout, s_bytes, q, qk_bytes) || overlap(S_inout, s_bytes, k, qk_bytes) ||
-        overlap(S_inout, s_bytes, v, v_bytes) || overlap(S_inout, s_bytes, o, v_bytes))
-        return fail(KDA_ERR_INVALID_ARG, "S_inout overlaps another argument");
+    const size_t gates = gate == KDA_GATE_HEAD ? H : rows * H;
+    if ((st = check_apart({{S_inout, s_bytes, "S_inout"}, {o, v_bytes, "o"}, {q, qk_bytes, "q"},
+                          {k, qk_bytes, "k"}, {v, v_bytes, "v"}, {log_g, gates * 4, "log_g"}}, 2)) !=
+        KDA_OK)
+        return st;
     kda::LinearParams p = linear_params(&d);
     p.q = q; p.k = k; p.v = v; p.log_g = log_g; p.o = o;
     p.h0 = p.hT = S_inout;   // each thread writes what it alone has read
@@ -1003,10 +1022,12 @@ kda_status_t kda_decode_tree(int N, int H, int T, kda_dtype_t dtype, const void*
         return st;
     if (!any) return KDA_OK;
     const size_t rows = (size_t)N * T * H, x = rows * 128 * (dtype == KDA_BF16 ? 2 : 4);
-    if (overlap(o, x, q, x) || overlap(o, x, k, x) || overlap(o, x, v, x) ||
-        overlap(o, x, log_g, rows * 512) || overlap(o, x, beta, x / 128) ||
-        overlap(o, x, parents, (size_t)N * T * 4) || overlap(o, x, S, (size_t)N * H * 65536))
-        return fail(KDA_ERR_INVALID_ARG, "o overlaps another argument");
+    if ((st = check_apart({{o, x, "o"}, {q, x, "q"}, {k, x, "k"}, {v, x, "v"},
+                          {log_g, rows * 512, "log_g"}, {beta, x / 128, "beta"},
+                          {parents, (size_t)N * T * 4, "parents"},
+                          {S, (size_t)N * H * 65536, "S"}}, 1)) !=
+        KDA_OK)
+        return st;
     kda::TreeParams p{q, k, v, log_g, beta, parents, const_cast<float*>(S), o, N, H, T, 0,
                       dtype == KDA_BF16, nullptr};
     if ((st = device_error_word(&p.err)) != KDA_OK) return st;
@@ -1028,11 +1049,11 @@ kda_status_t kda_commit_path(int N, int H, int T, int A, kda_dtype_t dtype, cons
         return st;
     if (!any) return KDA_OK;
     const size_t rows = (size_t)N * T * H, x = rows * 128 * (dtype == KDA_BF16 ? 2 : 4);
-    const size_t s = (size_t)N * H * 65536;
-    if (overlap(S_inout, s, k, x) || overlap(S_inout, s, v, x) ||
-        overlap(S_inout, s, log_g, rows * 512) || overlap(S_inout, s, beta, x / 128) ||
-        overlap(S_inout, s, path, (size_t)N * A * 4))
-        return fail(KDA_ERR_INVALID_ARG, "S_inout overlaps another argument");
+    if ((st = check_apart({{S_inout, (size_t)N * H * 65536, "S_inout"}, {k, x, "k"}, {v, x, "v"},
+                          {log_g, rows * 512, "log_g"}, {beta, x / 128, "beta"},
+                          {path, (size_t)N * A * 4, "path"}}, 1)) !=
+        KDA_OK)
+        return st;
     kda::TreeParams p{nullptr, k, v, log_g, beta, path, S_inout, nullptr, N, H, T, A,
                       dtype == KDA_BF16, nullptr};
     if ((st = device_error_word(&p.err)) != KDA_OK) return st;

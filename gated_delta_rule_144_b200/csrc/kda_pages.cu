@@ -9,6 +9,8 @@
 // each block checks its own pair against the whole list (8 bytes per pair from L2, small beside
 // its piece) and leaves a pair in conflict, or out of range, as it is, recording the error.
 
+#include <algorithm>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -60,10 +62,11 @@ page_copy_kernel(uint4* pool, const int32_t* __restrict__ src, const int32_t* __
 cudaError_t launch_page_copy(void* pool, const int32_t* src, const int32_t* dst, int n, int layers,
                              int pages, long long page_bytes, unsigned* err, cudaStream_t stream) {
     const long long vecs = page_bytes / 16;
-    // 32 KiB pieces (one pass of the block's loads); larger ones where there are blocks to spare
+    // 32 KiB pieces (one pass of the block's loads); 128 KiB where there are blocks to spare, and
+    // there as much as 4 times the list that every block reads
     long long piece = kThreads * kUnroll;
     const long long total = (long long)n * layers * ((vecs + piece - 1) / piece);
-    if (total > 148 * 32) piece *= 4;
+    if (total > 148 * 32) piece *= std::max(4ll, (2ll * n + piece - 1) / piece);
     const long long pieces = (vecs + piece - 1) / piece, blocks = pieces * n * layers;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     page_copy_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(

@@ -363,11 +363,13 @@ typedef struct {
  *
  *   q, k : [B, T, Hk, dk] dtype      v, o : [B, T, H, dv] dtype      log_g : see gate
  *   h0   : [N, H, dk, dv] float32 or NULL (zero)
- *   hT   : [N, H, dk, dv] float32 or NULL; must not overlap h0. o must not overlap q, k or v.
+ *   hT   : [N, H, dk, dv] float32 or NULL. o, hT and the workspace must not overlap one another
+ *          or any input.
  *   cu_seqlens : as for kda_fwd (B = 1; empty documents keep their initial state).
  *   workspace  : kda_linear_fwd_workspace_size(desc) bytes, 16-byte aligned (NULL when 0): the
  *                states between the segments that long sequences are cut into, and their decays.
- * Tokens of one document never reach another's outputs, whatever values they hold.
+ * Calls that may run at the same time need a workspace each. Tokens of one document never reach
+ * another's outputs, nor a token those before it, whatever values (infinities, NaN) they hold.
  */
 kda_status_t kda_linear_fwd(const kda_linear_desc_t* desc, const void* q, const void* k,
                             const void* v, const float* log_g, const float* h0,

@@ -45,6 +45,10 @@ def linear(L, h0=None, cu=None, ptr=None, ws=None, ws_bytes=0, **kw):
     (dict(ptr=dict(o=far(4) + 2)), INVALID), (dict(h0=far(6) + 4), INVALID),
     (dict(ptr=dict(o=far(2))), INVALID), (dict(ptr=dict(o=far(0) + 64)), INVALID),
     (dict(h0=far(5)), INVALID),
+    (dict(ptr=dict(o=far(3))), INVALID), (dict(ptr=dict(hT=far(1) + 128)), INVALID),
+    (dict(ptr=dict(hT=far(4) + 16)), INVALID), (dict(h0=far(6), ptr=dict(o=far(6))), INVALID),
+    (dict(T=4096, dtype=0, ws=far(2), ws_bytes=1 << 30), INVALID),
+    (dict(T=4096, dtype=0, ws=far(5) - 64, ws_bytes=1 << 30), INVALID),
 ], ids=str)
 def test_linear_fwd_refuses(L, kw, code):
     assert linear(L, **kw) == code
@@ -73,6 +77,7 @@ def test_linear_decode_refuses(L):
     assert call(dk=512) == UNSUPPORTED and call(dtype=9) == INVALID and call(gate=-1) == INVALID
     assert call(q=None) == INVALID and call(S=far(3) + 8) == INVALID
     assert call(S=far(0)) == INVALID and call(o=far(1)) == INVALID and call(S=far(4)) == INVALID
+    assert call(S=far(6)) == INVALID and call(o=far(6)) == INVALID
     assert call(N=0, q=None, S=None, o=None) == 0 and call(T=0, q=None) == 0
 
 
