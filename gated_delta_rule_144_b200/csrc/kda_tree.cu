@@ -184,11 +184,11 @@ struct TreeSmem {
     static constexpr int kN = kB * NB;
     // S, then the products: rows i of k d S, rows kN + i of q d S
     float state[2 * kN * kLd > kD * kD ? 2 * kN * kLd : kD * kD];
-    float frag[2 * kN * kD];             // the gates, then path products; then the left operand
+    // the gates, then path products; then the left operand; then u, [node][column]
+    float frag[2 * kN * kD];
     float k[kN * kLk];                   // k, then k / (path product)
     float akk[kN * kN], aqk[kN * kN];    // [j][i]: pairs of node i and j above it (and j = i)
-    float u[NB > 1 ? kB * kD : 4];       // the block of u that the blocks behind take
-    unsigned long long bad[NB > 1 ? kD : 1];
+    unsigned long long bad[kD];          // by column: nodes whose u is infinite or NaN
     unsigned long long above[2][kN];     // the nodes above each node
     int par[kN], jump[2][kN];
     float beta[kN];
@@ -232,6 +232,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int unit = blockIdx.x, n = unit / p.H, h = unit % p.H, T = p.T;
+    const int width = kD / gridDim.y, c0 = width * blockIdx.y;   // this block's value columns
     float* s_d = sm.frag;   // the gates, then the products over each node's path
     const Tin* q = static_cast<const Tin*>(p.q);
     const Tin* k = static_cast<const Tin*>(p.k);
@@ -241,8 +242,11 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 
     // this thread's pieces: node piece / 32, four channels; absent nodes hold k = q = 0, gate 1
     constexpr int kMine = kN * 32 / kThreads;
+    const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and group of nodes
+    const bool mine = col >= c0 && col < c0 + width;
     float4 qd[kMine], kd[kMine];
-    {   // (loads that wait for nothing; rows of absent nodes are dropped afterwards)
+    Tin vr[kB];
+    {   // all loads that wait for nothing, at once; rows of absent nodes are dropped afterwards
         float4 g[kMine];
         int par[kMine];
 #pragma unroll
@@ -253,13 +257,27 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             g[m] = load4(p.log_g + row(r) + 4 * lane);
             par[m] = p.nodes[(size_t)n * T + r];
         }
+        if (blk < NB && mine) {
+#pragma unroll
+            for (int i = 0; i < kB; ++i) vr[i] = v[row(min(kB * blk + i, T - 1)) + col];
+        }
+        const int own = min(tid, T - 1);
+        int parent = p.nodes[(size_t)n * T + own];
+        const float beta = load_elem(static_cast<const Tin*>(p.beta), ((int64_t)n * T + own) * p.H + h);
         if (tid == 0) {   // behind the rows, which are needed first
             mbar_init(bar, 1);
             fence_mbar_init();
-            mbar_arrive_expect_tx(bar, kStateBytes);
-            for (int i = 0; i < 4; ++i)
-                tma_load_2d(smem_u32(sm.state + i * kD * 32), &map, bar, 32 * i, unit * kD);
+            mbar_arrive_expect_tx(bar, kD * 4 * width);
+            for (int c = c0; c < c0 + width; c += 32)
+                tma_load_2d(smem_u32(sm.state + c * kD), &map, bar, c, unit * kD);
             sm.bad_tree = 0;
+        }
+        if (tid < kN) {
+            if (tid >= T) parent = -2;
+            sm.par[tid] = parent;
+            sm.jump[0][tid] = parent;
+            sm.above[0][tid] = parent >= 0 && parent < kN ? 1ull << parent : 0;
+            sm.beta[tid] = parent == -2 ? 0.f : beta;
         }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
@@ -273,21 +291,6 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             *reinterpret_cast<float4*>(s_d + r * kD + 4 * lane) = g[m];
             *reinterpret_cast<float4*>(sm.k + r * kLk + 4 * lane) = kd[m];
         }
-    }
-    const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and block of nodes
-    float y[kB], r[kB];
-    if (blk < NB) {
-#pragma unroll
-        for (int i = 0; i < kB; ++i) r[i] = load_elem(v, row(min(kB * blk + i, T - 1)) + col);
-    }
-    if (tid < kN) {
-        const int par = tid < T ? p.nodes[(size_t)n * T + tid] : -2;
-        sm.par[tid] = par;
-        sm.jump[0][tid] = par;
-        sm.above[0][tid] = par >= 0 && par < kN ? 1ull << par : 0;
-        sm.beta[tid] = par == -2 ? 0.f
-                                 : load_elem(static_cast<const Tin*>(p.beta),
-                                             ((int64_t)n * T + tid) * p.H + h);
     }
     __syncthreads();
     if (tid < T) {   // -2: no node; else the root or an earlier node that is there
@@ -338,7 +341,8 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
         const float4 d = load4(path + (m * kWarps + warp) * kD + 4 * lane), x = kd[m];
-        over[m] = make_float4(x.x / d.x, x.y / d.y, x.z / d.z, x.w / d.w);
+        over[m] = make_float4(__fdividef(x.x, d.x), __fdividef(x.y, d.y), __fdividef(x.z, d.z),
+                              __fdividef(x.w, d.w));   // (2 units in the last place, d is not steep)
         kd[m] = mul4(x, d);
         qd[m] = mul4(qd[m], d);
         auto size = [](float4 a) { return (fabsf(a.x) + fabsf(a.y)) + (fabsf(a.z) + fabsf(a.w)); };
@@ -378,15 +382,16 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             at0[e] = state_at(lane & 3, cols + 16 * e + 2 * (lane >> 2));
             at1[e] = state_at((lane & 3) + 4, cols + 16 * e + 2 * (lane >> 2));
         }
-        float c0[2 * NB][kN8][4], c1[2 * NB][kN8][4];
+        const bool own = cols >= c0 && cols < c0 + width;
+        float a0[2 * NB][kN8][4], a1[2 * NB][kN8][4];
 #pragma unroll
         for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
             for (int e = 0; e < kN8; ++e)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) c0[b][e][x] = c1[b][e][x] = 0.f;
+                for (int x = 0; x < 4; ++x) a0[b][e][x] = a1[b][e][x] = 0.f;
 #pragma unroll 2
-        for (int ks = 0; ks < 16; ++ks) {
+        for (int ks = 0; ks < 16 && own; ++ks) {
             float2 s0[kN8], s1[kN8];
 #pragma unroll
             for (int e = 0; e < kN8; ++e) {
@@ -398,19 +403,22 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
                 const float4 f = load_frag(sm.frag + b * 2048, ks, lane);
 #pragma unroll
                 for (int e = 0; e < kN8; ++e)
-                    mma_step<sizeof(Tin) == 4>(c0[b][e], c1[b][e], f, s0[e], s1[e]);
+                    mma_step<sizeof(Tin) == 4>(a0[b][e], a1[b][e], f, s0[e], s1[e]);
             }
         }
         bar_sync(1, kThreads / 2);   // S has been read
 #pragma unroll
-        for (int b = 0; b < 2 * NB; ++b)
+        for (int b = 0; b < 2 * NB && own; ++b)
 #pragma unroll
             for (int e = 0; e < kN8; ++e)
-                store_tile(sm.state + kB * b * kLd, cols + 16 * e, lane, c0[b][e], c1[b][e]);
+                store_tile(sm.state + kB * b * kLd, cols + 16 * e, lane, a0[b][e], a1[b][e]);
     } else if (!steep) {   // tile (16 rows of [k d; q d]) x (8 nodes)
 #pragma unroll 1
         for (int tile = warp - kWarps / 2; tile < 4 * NB * NB; tile += kWarps / 2) {
-            const int mt = tile / (2 * NB), nt = tile % (2 * NB);
+            // (places shifted by the row tile, so that each warp has as many of the tiles with
+            // nodes up to its rows)
+            const int mt = tile / (2 * NB), nt = (tile + mt) % (2 * NB);
+            if (nt > 2 * (mt % NB) + 1) continue;
             float c[4] = {0.f, 0.f, 0.f, 0.f};
             const float* b = sm.k + (8 * nt + (lane >> 2)) * kLk + (lane & 3);
 #pragma unroll 4
@@ -429,47 +437,65 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     }
     __syncthreads();
 
-    if (blk < NB) {
+    // The substitution for u: group b of 128 threads, one per column, solves block b in registers
+    // while the others add the block before to their read-outs; then the groups behind take its u.
+    float* s_u = sm.frag;
+    float r[kB];
+    if (blk < NB && mine) {
 #pragma unroll
-        for (int i = 0; i < kB; ++i) {
-            r[i] = sm.par[kB * blk + i] != -2 ? r[i] - sm.state[(kB * blk + i) * kLd + col] : 0.f;
-            y[i] = sm.state[(kN + kB * blk + i) * kLd + col];
-        }
+        for (int i = 0; i < kB; ++i)
+            r[i] = sm.par[kB * blk + i] != -2
+                       ? load_elem(vr, i) - sm.state[(kB * blk + i) * kLd + col] : 0.f;
     }
-    // r and y less what node (b, j)'s u adds to the rows e of block `to`, first <= e
+    // r less what node `at`'s u adds to the rows e of block `to`, first <= e
     auto spread = [&](int at, int to, float u, int first) {
-        const float *ak = sm.akk + at * kN + kB * to, *aq = sm.aqk + at * kN + kB * to;
+        const float* ak = sm.akk + at * kN + kB * to;
 #pragma unroll
         for (int i4 = 0; i4 < kB; i4 += 4) {
             if (i4 + 3 < first) continue;
-            const float4 a = load4(ak + i4), c = load4(aq + i4);
-            const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
+            const float4 a = load4(ak + i4);
+            const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (i4 + e >= first) {
-                    r[i4 + e] = fmaf(-av[e], u, r[i4 + e]);
-                    y[i4 + e] = fmaf(cv[e], u, y[i4 + e]);
-                }
+                if (i4 + e >= first) r[i4 + e] = fmaf(-av[e], u, r[i4 + e]);
         }
     };
-    Tin* o = static_cast<Tin*>(p.o);
-    unsigned long long bad = 0;   // nodes whose u is infinite or NaN in this column
-    for (int b = 0; b < NB; ++b) {
-        if (blk == b) {
-            if (NB > 1 && b > 0) bad = sm.bad[col];
-            float finite = 0.f;
-            float* rs = sm.state + kB * b * kLd + col;           // r and y as they are, kept in
-            float* ys = sm.state + (kN + kB * b) * kLd + col;    // the products' places
+    // the thread's read-outs, rows y0 .. y0 + kY - 1: y plus what block b's u adds to them
+    constexpr int kY = kThreads == kD * NB ? kB : kN * kD / kThreads;
+    const int y0 = kY * blk;
+    float y[kY];
+    if (mine) {
 #pragma unroll
-            for (int j = 0; j < kB; ++j) rs[j * kLd] = r[j], ys[j * kLd] = y[j];
+        for (int i = 0; i < kY; ++i) y[i] = sm.state[(kN + y0 + i) * kLd + col];
+    }
+    auto read_out = [&](int b) {
+        const float *u = s_u + kB * b * kD + col, *aq = sm.aqk + kB * b * kN + y0;
+#pragma unroll 4
+        for (int j = 0; j < kB; ++j) {
+            const float x = u[j * kD];
+#pragma unroll
+            for (int i = 0; i < kY; i += 4) {
+                const float4 c = load4(aq + j * kN + i);
+                y[i] = fmaf(c.x, x, y[i]), y[i + 1] = fmaf(c.y, x, y[i + 1]);
+                y[i + 2] = fmaf(c.z, x, y[i + 2]), y[i + 3] = fmaf(c.w, x, y[i + 3]);
+            }
+        }
+    };
+#pragma unroll 1
+    for (int b = 0; b < NB && mine; ++b) {
+        if (blk == b) {
+            unsigned long long bad = b > 0 ? sm.bad[col] : 0;
+            float finite = 0.f;
+            float* rs = sm.state + kB * b * kLd + col;   // r as it is, in the product's place
+#pragma unroll
+            for (int j = 0; j < kB; ++j) rs[j * kLd] = r[j];
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
                 const int at = kB * b + j;
                 const float u = sm.beta[at] * r[j];
                 finite = fmaf(u, 0.f, finite);
-                y[j] = fmaf(sm.aqk[at * kN + at], u, y[j]);
                 spread(at, b, u, j + 1);
-                if (NB > 1) sm.u[j * kD + col] = u;
+                s_u[at * kD + col] = u;
             }
             if (bad != 0 || finite != 0.f) {
                 // The pairs of other branches have coefficient 0. An infinite or NaN u turned that
@@ -478,38 +504,37 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 #pragma unroll 1
                 for (int j = 0; j < kB; ++j) {
                     const int at = kB * b + j;
-                    const float *ak = sm.akk + at * kN + kB * b, *aq = sm.aqk + at * kN + kB * b;
-                    float u = bad & s_above[at] ? __int_as_float(0x7fc00000)
-                                                 : sm.beta[at] * rs[j * kLd];
-                    ys[j * kLd] = fmaf(aq[j], u, ys[j * kLd]);
-                    if (!(fabsf(u) <= 3.402823466e38f)) {
+                    const float* ak = sm.akk + at * kN + kB * b;
+                    float u = sm.beta[at] * rs[j * kLd];
+                    if (bad & s_above[at] || !(fabsf(u) <= 3.402823466e38f)) {
                         u = 0.f;
                         bad |= 1ull << at;
                     }
-                    if (NB > 1) sm.u[j * kD + col] = u;
+                    s_u[at * kD + col] = u;
 #pragma unroll 1
-                    for (int e = j + 1; e < kB; ++e) {
-                        rs[e * kLd] = fmaf(-ak[e], u, rs[e * kLd]);
-                        ys[e * kLd] = fmaf(aq[e], u, ys[e * kLd]);
-                    }
+                    for (int e = j + 1; e < kB; ++e) rs[e * kLd] = fmaf(-ak[e], u, rs[e * kLd]);
                 }
-#pragma unroll
-                for (int j = 0; j < kB; ++j) y[j] = ys[j * kLd];
             }
-            if (NB > 1) sm.bad[col] = bad;
-#pragma unroll
-            for (int j = 0; j < kB; ++j)
-                if (sm.par[kB * b + j] != -2) store_elem(o, row(kB * b + j) + col, y[j]);
+            sm.bad[col] = bad;
+        } else if (NB > 1 && b > 0 && blk >= b - 1) {
+            if (blk == b - 1 && blk > 0) read_out(blk - 1);   // (put off while it solved)
+            read_out(b - 1);
         }
-        if (NB > 1 && b + 1 < NB) {
-            __syncthreads();
-            if (blk > b && blk < NB) {
+        bar_sync(1, NB == 1 ? 2 * width : NB * width);
+        if (blk > b && blk < NB) {
 #pragma unroll 4
-                for (int j = 0; j < kB; ++j) spread(kB * b + j, blk, sm.u[j * kD + col], 0);
-            }
-            __syncthreads();
+            for (int j = 0; j < kB; ++j) spread(kB * b + j, blk, s_u[(kB * b + j) * kD + col], 0);
         }
     }
+    if (!mine) return;
+    if (NB > 1 && blk == NB - 1) read_out(NB - 2);
+    if (blk == NB - 1 || NB == 1) read_out(NB - 1);
+    Tin* o = static_cast<Tin*>(p.o);
+    const unsigned long long bad = sm.bad[col];
+#pragma unroll
+    for (int i = 0; i < kY; ++i)
+        if (sm.par[y0 + i] != -2)
+            store_elem(o, row(y0 + i) + col, bad >> (y0 + i) & 1 ? __int_as_float(0x7fc00000) : y[i]);
 }
 
 // The commit. Two blocks per SM walk the (sequence, head) units: four warps work on one unit's state
@@ -776,31 +801,33 @@ cudaError_t set_up(int dev) {
 }
 
 template <typename Tin, int NB>
-cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
+cudaError_t launch_tree(const TreeParams& p, int sms, cudaStream_t stream) {
     CUtensorMap map;
     const cudaError_t e = make_map_2d(&map, p.S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
                                       (unsigned long long)p.N * p.H * kD, kD, 32, kD,
                                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.N * p.H), p.N * p.H * 2 <= sms ? 2 : 1);
     decode_tree_kernel<Tin, NB>
-        <<<(unsigned)(p.N * p.H), tree_threads(NB), sizeof(TreeSmem<Tin, NB>), stream>>>(map, p);
+        <<<grid, tree_threads(NB), sizeof(TreeSmem<Tin, NB>), stream>>>(map, p);
     return cudaGetLastError();
 }
 
 template <typename Tin>
-cudaError_t launch_tree_nodes(const TreeParams& p, cudaStream_t stream) {
-    if (p.T <= 16) return launch_tree<Tin, 1>(p, stream);
-    if (p.T <= 32) return launch_tree<Tin, 2>(p, stream);
-    return launch_tree<Tin, 4>(p, stream);
+cudaError_t launch_tree_nodes(const TreeParams& p, int sms, cudaStream_t stream) {
+    if (p.T <= 16) return launch_tree<Tin, 1>(p, sms, stream);
+    if (p.T <= 32) return launch_tree<Tin, 2>(p, sms, stream);
+    return launch_tree<Tin, 4>(p, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
-    const cudaError_t e = g_setup.run(set_up);
+    int dev = 0;
+    const cudaError_t e = g_setup.run(set_up, &dev);
     if (e != cudaSuccess) return e;
-    return p.bf16 ? launch_tree_nodes<__nv_bfloat16>(p, stream)
-                  : launch_tree_nodes<float>(p, stream);
+    return p.bf16 ? launch_tree_nodes<__nv_bfloat16>(p, g_sms[dev], stream)
+                  : launch_tree_nodes<float>(p, g_sms[dev], stream);
 }
 
 cudaError_t launch_commit_path(const TreeParams& p, cudaStream_t stream) {
