@@ -14,7 +14,7 @@
 // one per SM, above). Phases:
 //   load     S by TMA into shared memory, under way until the product; the rows of k and the
 //            gates.
-//   paths    d_i of every node in log2(depth) rounds that each double the stretch of path covered.
+//   paths    d_i of every node, one after another: a thread per channel, no barrier between them.
 //   pairs    d_ij = d_i / d_j, so all pairs are one product [k d; q d] (k / d)^T on the tensor
 //            cores, of which the tree keeps its own. Where some d is below 1e-20 (a gate of -inf
 //            included) the quotient leaves the range: then a warp per node walks the node's
@@ -189,8 +189,8 @@ struct TreeSmem {
     float k[kN * kLk];                   // k, then k / (path product)
     float akk[kN * kN], aqk[kN * kN];    // [j][i]: pairs of node i and j above it (and j = i)
     unsigned long long bad[kD];          // by column: nodes whose u is infinite or NaN
-    unsigned long long above[2][kN];     // the nodes above each node
-    int par[kN], jump[2][kN];
+    unsigned long long above[kN];        // the nodes above each node
+    alignas(16) int par[kN];
     float beta[kN];
     unsigned long long bar;
     int bad_tree;
@@ -237,7 +237,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     const Tin* q = static_cast<const Tin*>(p.q);
     const Tin* k = static_cast<const Tin*>(p.k);
     const Tin* v = static_cast<const Tin*>(p.v);
-    auto row = [&](int i) { return (((size_t)n * T + i) * p.H + h) * kD; };
+    const size_t first = ((size_t)n * T * p.H + h) * kD, stride = (size_t)p.H * kD;   // of rows
     const uint32_t bar = smem_u32(&sm.bar);
 
     // this thread's pieces: node piece / 32, four channels; absent nodes hold k = q = 0, gate 1
@@ -252,32 +252,28 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
             const int r = min(m * kWarps + warp, T - 1);
-            kd[m] = load4(k + row(r) + 4 * lane);
-            qd[m] = load4(q + row(r) + 4 * lane);
-            g[m] = load4(p.log_g + row(r) + 4 * lane);
+            const size_t at = first + r * stride + 4 * lane;
+            kd[m] = load4(k + at);
+            qd[m] = load4(q + at);
+            g[m] = load4(p.log_g + at);
             par[m] = p.nodes[(size_t)n * T + r];
         }
         if (blk < NB && mine) {
+            const Tin* at = v + first + kB * blk * stride + col;
 #pragma unroll
-            for (int i = 0; i < kB; ++i) vr[i] = v[row(min(kB * blk + i, T - 1)) + col];
+            for (int i = 0; i < kB; ++i, at += stride)
+                if (kB * blk + i < T) vr[i] = *at;
         }
-        const int own = min(tid, T - 1);
+        const int node = tid - kThreads / 2, own = min(max(node, 0), T - 1);
         int parent = p.nodes[(size_t)n * T + own];
-        const float beta = load_elem(static_cast<const Tin*>(p.beta), ((int64_t)n * T + own) * p.H + h);
-        if (tid == 0) {   // behind the rows, which are needed first
+        const Tin beta = static_cast<const Tin*>(p.beta)[((int64_t)n * T + own) * p.H + h];
+        if (tid == kThreads - 32) {   // behind the rows, which are needed first
             mbar_init(bar, 1);
             fence_mbar_init();
             mbar_arrive_expect_tx(bar, kD * 4 * width);
             for (int c = c0; c < c0 + width; c += 32)
                 tma_load_2d(smem_u32(sm.state + c * kD), &map, bar, c, unit * kD);
             sm.bad_tree = 0;
-        }
-        if (tid < kN) {
-            if (tid >= T) parent = -2;
-            sm.par[tid] = parent;
-            sm.jump[0][tid] = parent;
-            sm.above[0][tid] = parent >= 0 && parent < kN ? 1ull << parent : 0;
-            sm.beta[tid] = parent == -2 ? 0.f : beta;
         }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
@@ -291,6 +287,11 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             *reinterpret_cast<float4*>(s_d + r * kD + 4 * lane) = g[m];
             *reinterpret_cast<float4*>(sm.k + r * kLk + 4 * lane) = kd[m];
         }
+        if (node >= 0 && node < kN) {
+            if (node >= T) parent = -2;
+            sm.par[node] = parent;
+            sm.beta[node] = parent == -2 ? 0.f : load_elem(&beta, 0);
+        }
     }
     __syncthreads();
     if (tid < T) {   // -2: no node; else the root or an earlier node that is there
@@ -299,43 +300,63 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     }
     __syncthreads();
     if (sm.bad_tree) {   // (the copy lands before its shared memory goes away)
-        if (tid == 0) {
+        if (tid == kThreads - 32) {
             set_device_error(p.err, DEV_BAD_INDEX);
             mbar_wait(bar, 0, kWaitCycles);
         }
         return;
     }
 
-    // paths: each round multiplies a node's product by that of the node its path has reached, and
-    // reaches twice as far (two places for the products and the jumps, taken in turn)
+    // paths, in the nodes' order, four at a time: a thread per channel multiplies each node's gate by
+    // its parent's product, which it has in a register or wrote itself, so nothing waits for another
+    // thread; one more thread gathers the nodes above each node the same way
     bool steep = false;
-    int at = 0;
-#pragma unroll 1
-    for (bool more = true; more; at ^= 1) {
-        const float* from = s_d + at * kN * kD;
-        float* to = s_d + (at ^ 1) * kN * kD;
+    if (tid < kD) {
+        int4 next = *reinterpret_cast<const int4*>(sm.par);
+        float ng[4];
 #pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-            const int i = m * kWarps + warp, j = sm.jump[at][i];
-            float4 d = load4(from + i * kD + 4 * lane);
-            if (j >= 0) d = mul4(d, load4(from + j * kD + 4 * lane));
-            *reinterpret_cast<float4*>(to + i * kD + 4 * lane) = d;
-        }
-        int far = -1;
-        if (tid < kN) {
-            const int j = sm.jump[at][tid];
-            unsigned long long above = sm.above[at][tid];
-            if (j >= 0) {
-                above |= sm.above[at][j];
-                far = sm.jump[at][j];
+        for (int e = 0; e < 4; ++e) ng[e] = s_d[e * kD + tid];
+#pragma unroll 1
+        for (int i = 0; i < kN; i += 4) {
+            const int j[4] = {next.x, next.y, next.z, next.w};
+            float x[4], d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[e] = ng[e];
+                x[e] = j[e] >= 0 && j[e] < i ? s_d[j[e] * kD + tid] : 1.f;
             }
-            sm.jump[at ^ 1][tid] = far;
-            sm.above[at ^ 1][tid] = above;
+            const int i2 = min(i + 4, kN - 4);
+            next = *reinterpret_cast<const int4*>(sm.par + i2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ng[e] = s_d[(i2 + e) * kD + tid];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int m = 0; m < e; ++m) x[e] = j[e] == i + m ? d[m] : x[e];
+                d[e] *= x[e];
+                s_d[(i + e) * kD + tid] = d[e];
+            }
         }
-        more = __syncthreads_or(far >= 0);
+    } else if (tid == kD) {
+#pragma unroll 1
+        for (int i = 0; i < kN; i += 4) {
+            const int4 par = *reinterpret_cast<const int4*>(sm.par + i);
+            const int j[4] = {par.x, par.y, par.z, par.w};
+            unsigned long long x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = j[e] >= 0 && j[e] < i ? sm.above[j[e]] : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int m = 0; m < e; ++m) x[e] = j[e] == i + m ? x[m] : x[e];
+                if (j[e] >= 0) x[e] |= 1ull << j[e];
+                sm.above[i + e] = x[e];
+            }
+        }
     }
-    const float* path = s_d + at * kN * kD;
-    const unsigned long long* s_above = sm.above[at];
+    __syncthreads();
+    const float* path = s_d;
+    const unsigned long long* s_above = sm.above;
     // the left operand's rows k d and q d; k / d for the pairs
     float4 over[kMine];
 #pragma unroll
@@ -529,12 +550,12 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     if (!mine) return;
     if (NB > 1 && blk == NB - 1) read_out(NB - 2);
     if (blk == NB - 1 || NB == 1) read_out(NB - 1);
-    Tin* o = static_cast<Tin*>(p.o);
+    Tin* o = static_cast<Tin*>(p.o) + first + y0 * stride + col;
     const unsigned long long bad = sm.bad[col];
 #pragma unroll
-    for (int i = 0; i < kY; ++i)
+    for (int i = 0; i < kY; ++i, o += stride)
         if (sm.par[y0 + i] != -2)
-            store_elem(o, row(y0 + i) + col, bad >> (y0 + i) & 1 ? __int_as_float(0x7fc00000) : y[i]);
+            store_elem(o, 0, bad >> (y0 + i) & 1 ? __int_as_float(0x7fc00000) : y[i]);
 }
 
 // The commit. Two blocks per SM walk the (sequence, head) units: four warps work on one unit's state
