@@ -56,6 +56,20 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
                        __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
+// Four elements as they are in memory, and their values.
+template <typename Tin>
+struct Raw4 {
+    using type = float4;
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    using type = uint2;
+};
+__device__ __forceinline__ float4 widen(float4 x) { return x; }
+__device__ __forceinline__ float4 widen(uint2 u) {
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
 __device__ __forceinline__ float dot4(float4 a, float4 b) {
     return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
 }
@@ -245,7 +259,13 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and group of nodes
     const bool mine = col >= c0 && col < c0 + width;
     float4 qd[kMine], kd[kMine];
-    Tin vr[kB];
+    // half of the warps take the products with S, kCols columns each, whose sums for the rows k d
+    // start from -v
+    constexpr int kCols = kD / (kWarps / 2), kN8 = kCols / 16;   // columns, pairs of 8 of them
+    const int cols = kCols * warp;
+    const bool own = cols >= c0 && cols < c0 + width;
+    using Raw = typename Raw4<Tin>::type;
+    Raw vr[NB][kN8][2];
     {   // all loads that wait for nothing, at once; rows of absent nodes are dropped afterwards
         float4 g[kMine];
         int par[kMine];
@@ -258,11 +278,19 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             g[m] = load4(p.log_g + at);
             par[m] = p.nodes[(size_t)n * T + r];
         }
-        if (blk < NB && mine) {
-            const Tin* at = v + first + kB * blk * stride + col;
+        if (warp < kWarps / 2) {
 #pragma unroll
-            for (int i = 0; i < kB; ++i, at += stride)
-                if (kB * blk + i < T) vr[i] = *at;
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < kN8; ++e)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int r = kB * b + (lane >> 2) + 8 * x;
+                        vr[b][e][x] = Raw{};
+                        if (r < T && own)
+                            vr[b][e][x] = *reinterpret_cast<const Raw*>(
+                                v + first + r * stride + cols + 16 * e + 4 * (lane & 3));
+                    }
         }
         const int node = tid - kThreads / 2, own = min(max(node, 0), T - 1);
         int parent = p.nodes[(size_t)n * T + own];
@@ -309,7 +337,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 
     // paths, in the nodes' order, four at a time: a thread per channel multiplies each node's gate by
     // its parent's product, which it has in a register or wrote itself, so nothing waits for another
-    // thread; one more thread gathers the nodes above each node the same way
+    // thread; another warp gathers the nodes above each node, reaching twice as far each round
     bool steep = false;
     if (tid < kD) {
         int4 next = *reinterpret_cast<const int4*>(sm.par);
@@ -337,22 +365,35 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
                 s_d[(i + e) * kD + tid] = d[e];
             }
         }
-    } else if (tid == kD) {
-#pragma unroll 1
-        for (int i = 0; i < kN; i += 4) {
-            const int4 par = *reinterpret_cast<const int4*>(sm.par + i);
-            const int j[4] = {par.x, par.y, par.z, par.w};
-            unsigned long long x[4];
+    } else if (warp == kD / 32) {
+        constexpr int kPer = kN > 32 ? 2 : 1;   // nodes per lane: lane, lane + 32
+        int j[kPer];
+        unsigned long long x[kPer];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = j[e] >= 0 && j[e] < i ? sm.above[j[e]] : 0;
+        for (int e = 0; e < kPer; ++e) {
+            j[e] = lane + 32 * e < kN ? sm.par[lane + 32 * e] : -1;
+            x[e] = j[e] >= 0 ? 1ull << j[e] : 0;
+        }
+        auto of = [&](const auto& y, int i) {   // node i's
+            const auto lo = __shfl_sync(0xffffffffu, y[0], i & 31);
+            if (kPer == 1) return lo;
+            const auto hi = __shfl_sync(0xffffffffu, y[kPer - 1], i & 31);
+            return i < 32 ? lo : hi;
+        };
+        while (__any_sync(0xffffffffu, j[0] >= 0 || j[kPer - 1] >= 0)) {
+            int far[kPer];
+            unsigned long long more[kPer];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kPer; ++e) far[e] = of(j, j[e]), more[e] = of(x, j[e]);
 #pragma unroll
-                for (int m = 0; m < e; ++m) x[e] = j[e] == i + m ? x[m] : x[e];
-                if (j[e] >= 0) x[e] |= 1ull << j[e];
-                sm.above[i + e] = x[e];
+            for (int e = 0; e < kPer; ++e) {
+                x[e] |= j[e] >= 0 ? more[e] : 0;
+                j[e] = j[e] >= 0 ? far[e] : -1;
             }
         }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            if (lane + 32 * e < kN) sm.above[lane + 32 * e] = x[e];
     }
     __syncthreads();
     const float* path = s_d;
@@ -392,25 +433,26 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     if (!ok) set_device_error(p.err, DEV_TIMEOUT);
     if (__syncthreads_or(!ok)) return;
 
-    // half of the warps take the products with S (all 2 NB tiles of their columns, so that S is read
-    // once), the others the pairs
+    // the products with S (all 2 NB tiles of a warp's columns, so that S is read once) beside the pairs
     if (warp < kWarps / 2) {
-        constexpr int kCols = kD / (kWarps / 2), kN8 = kCols / 16;   // columns, pairs of 8 of them
-        const int cols = kCols * warp;
         int at0[kN8], at1[kN8];
 #pragma unroll
         for (int e = 0; e < kN8; ++e) {
             at0[e] = state_at(lane & 3, cols + 16 * e + 2 * (lane >> 2));
             at1[e] = state_at((lane & 3) + 4, cols + 16 * e + 2 * (lane >> 2));
         }
-        const bool own = cols >= c0 && cols < c0 + width;
         float a0[2 * NB][kN8][4], a1[2 * NB][kN8][4];
 #pragma unroll
         for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
             for (int e = 0; e < kN8; ++e)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) a0[b][e][x] = a1[b][e][x] = 0.f;
+                for (int x = 0; x < 2; ++x) {   // (a tile's four columns as store_tile has them)
+                    const float4 y = b < NB ? widen(vr[b < NB ? b : 0][e][x])
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                    a0[b][e][2 * x] = -y.x, a1[b][e][2 * x] = -y.y;
+                    a0[b][e][2 * x + 1] = -y.z, a1[b][e][2 * x + 1] = -y.w;
+                }
 #pragma unroll 2
         for (int ks = 0; ks < 16 && own; ++ks) {
             float2 s0[kN8], s1[kN8];
@@ -466,7 +508,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 #pragma unroll
         for (int i = 0; i < kB; ++i)
             r[i] = sm.par[kB * blk + i] != -2
-                       ? load_elem(vr, i) - sm.state[(kB * blk + i) * kLd + col] : 0.f;
+                       ? -sm.state[(kB * blk + i) * kLd + col] : 0.f;
     }
     // r less what node `at`'s u adds to the rows e of block `to`, first <= e
     auto spread = [&](int at, int to, float u, int first) {
