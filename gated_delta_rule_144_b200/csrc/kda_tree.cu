@@ -434,7 +434,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     if (__syncthreads_or(!ok)) return;
 
     // the products with S (all 2 NB tiles of a warp's columns, so that S is read once) beside the pairs
-    if (warp < kWarps / 2) {
+    if (warp < kWarps / 2 && own) {
         int at0[kN8], at1[kN8];
 #pragma unroll
         for (int e = 0; e < kN8; ++e) {
@@ -454,7 +454,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
                     a0[b][e][2 * x + 1] = -y.z, a1[b][e][2 * x + 1] = -y.w;
                 }
 #pragma unroll 2
-        for (int ks = 0; ks < 16 && own; ++ks) {
+        for (int ks = 0; ks < 16; ++ks) {
             float2 s0[kN8], s1[kN8];
 #pragma unroll
             for (int e = 0; e < kN8; ++e) {
@@ -469,32 +469,36 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
                     mma_step<sizeof(Tin) == 4>(a0[b][e], a1[b][e], f, s0[e], s1[e]);
             }
         }
-        bar_sync(1, kThreads / 2);   // S has been read
+        bar_sync(1, 32 * width / kCols);   // S has been read
 #pragma unroll
-        for (int b = 0; b < 2 * NB && own; ++b)
+        for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
             for (int e = 0; e < kN8; ++e)
                 store_tile(sm.state + kB * b * kLd, cols + 16 * e, lane, a0[b][e], a1[b][e]);
-    } else if (!steep) {   // tile (16 rows of [k d; q d]) x (8 nodes)
+    } else if (!steep) {
+        // tiles (16 rows of k d or q d, block b) x (8 nodes of the blocks up to b)
+        const int workers = kWarps - width / kCols, before = c0 / kCols;
+        constexpr int kTiles = NB * (NB + 1);   // of k d; as many of q d
 #pragma unroll 1
-        for (int tile = warp - kWarps / 2; tile < 4 * NB * NB; tile += kWarps / 2) {
-            // (places shifted by the row tile, so that each warp has as many of the tiles with
-            // nodes up to its rows)
-            const int mt = tile / (2 * NB), nt = (tile + mt) % (2 * NB);
-            if (nt > 2 * (mt % NB) + 1) continue;
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int tile = warp < kWarps / 2 && warp < before ? warp : warp - width / kCols;
+             tile < 2 * kTiles; tile += workers) {
+            const int half = tile / kTiles;
+            int nt = tile % kTiles, blk = 0;
+            while (nt >= 2 * (blk + 1)) nt -= 2 * ++blk;
+            float c[2][4] = {};   // sums of even and odd steps
             const float* b = sm.k + (8 * nt + (lane >> 2)) * kLk + (lane & 3);
-#pragma unroll 4
+            const float* a = sm.frag + (half * NB + blk) * 2048;
+#pragma unroll 8
             for (int ks = 0; ks < 16; ++ks)
-                mma_step<sizeof(Tin) == 4>(c, load_frag(sm.frag + mt * 2048, ks, lane), b[8 * ks],
+                mma_step<sizeof(Tin) == 4>(c[ks & 1], load_frag(a, ks, lane), b[8 * ks],
                                            b[8 * ks + 4]);
-            float* to = mt < NB ? sm.akk : sm.aqk;
+            float* to = half ? sm.aqk : sm.akk;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {   // rows g, g + 8; nodes 2 t, 2 t + 1
-                const int i = 16 * (mt % NB) + (lane >> 2) + 8 * (e >> 1);
+                const int i = 16 * blk + (lane >> 2) + 8 * (e >> 1);
                 const int j = 8 * nt + 2 * (lane & 3) + (e & 1);
-                const bool pair = (s_above[i] >> j & 1) || (mt >= NB && i == j);
-                to[j * kN + i] = pair ? c[e] : 0.f;
+                const bool pair = (s_above[i] >> j & 1) || (half && i == j);
+                to[j * kN + i] = pair ? c[0][e] + c[1][e] : 0.f;
             }
         }
     }
@@ -544,6 +548,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             }
         }
     };
+    int done = 0;   // blocks in the read-outs
 #pragma unroll 1
     for (int b = 0; b < NB && mine; ++b) {
         if (blk == b) {
@@ -552,14 +557,17 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             float* rs = sm.state + kB * b * kLd + col;   // r as it is, in the product's place
 #pragma unroll
             for (int j = 0; j < kB; ++j) rs[j * kLd] = r[j];
+            float u[kB];   // (stored at the end, so that no load waits for a store)
+#pragma unroll
+            for (int j = 0; j < kB; ++j) u[j] = sm.beta[kB * b + j];
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
-                const int at = kB * b + j;
-                const float u = sm.beta[at] * r[j];
-                finite = fmaf(u, 0.f, finite);
-                spread(at, b, u, j + 1);
-                s_u[at * kD + col] = u;
+                u[j] *= r[j];
+                finite = fmaf(u[j], 0.f, finite);
+                spread(kB * b + j, b, u[j], j + 1);
             }
+#pragma unroll
+            for (int j = 0; j < kB; ++j) s_u[(kB * b + j) * kD + col] = u[j];
             if (bad != 0 || finite != 0.f) {
                 // The pairs of other branches have coefficient 0. An infinite or NaN u turned that
                 // into NaN: again, with such a u entering the sums as 0. What is below its node in
@@ -579,9 +587,8 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
                 }
             }
             sm.bad[col] = bad;
-        } else if (NB > 1 && b > 0 && blk >= b - 1) {
-            if (blk == b - 1 && blk > 0) read_out(blk - 1);   // (put off while it solved)
-            read_out(b - 1);
+        } else if (done < b && done <= blk) {   // (one block at a time: no longer than the solve)
+            read_out(done++);
         }
         bar_sync(1, NB == 1 ? 2 * width : NB * width);
         if (blk > b && blk < NB) {
@@ -590,8 +597,8 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
         }
     }
     if (!mine) return;
-    if (NB > 1 && blk == NB - 1) read_out(NB - 2);
-    if (blk == NB - 1 || NB == 1) read_out(NB - 1);
+#pragma unroll 1
+    while (done <= min(blk, NB - 1)) read_out(done++);
     Tin* o = static_cast<Tin*>(p.o) + first + y0 * stride + col;
     const unsigned long long bad = sm.bad[col];
 #pragma unroll
