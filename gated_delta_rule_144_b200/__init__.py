@@ -119,7 +119,7 @@ def lib():
     L.kda_linear_fwd_workspace_size.restype = sz
     L.kda_linear_decode.argtypes = [i32] * 8 + [p] * 7
     L.kda_linear_decode.restype = i32
-    L.kda_decode_tree.argtypes = [i32] * 4 + [p] * 9
+    L.kda_decode_tree.argtypes = [i32] * 4 + [p] * 8 + [i32, p]
     L.kda_decode_tree.restype = i32
     L.kda_commit_path.argtypes = [i32] * 5 + [p] * 7
     L.kda_commit_path.restype = i32
@@ -704,22 +704,21 @@ def decode_tree(q, k, v, log_g, beta, parents, S, *, o=None, stream=None):
 
     q, k, v: [N, T, H, 128] (bf16 or fp32), log_g: fp32 alike, beta: [N, T, H], T <= 64. parents:
     int32 [N, T], -1 for a child of the committed state, else an earlier node, or -2 for no node:
-    o keeps that row (a new o holds zeros there). Returns o [N, T, H, 128]. Rejected parents leave
-    their sequence's rows and set KDA_ERR_BAD_INDEX (``get_device_error``).
+    o keeps that row (a new o holds zeros there). Returns o [N, T, H, 128]. A sequence with other
+    parents has no nodes and sets KDA_ERR_BAD_INDEX (``get_device_error``).
     """
     lib()
     dev, dt, N, T, H = _tree_rows(k, v, log_g, beta, S)
     _dev(q, "q", dt, k.shape, dev)
     _dev(parents, "parents", torch.int32, (N, T), dev)
-    if o is None:
+    clear = o is None
+    if clear:
         o = _empty(k, None, None, stream)
-        with torch.cuda.stream(stream):   # (None: the current one)
-            o.zero_()
     else:
         _dev(o, "o", dt, k.shape, dev)
     _call(lib().kda_decode_tree, "kda_decode_tree", dev, N, H, T, _dtype_code(k), q.data_ptr(),
           k.data_ptr(), v.data_ptr(), log_g.data_ptr(), beta.data_ptr(), parents.data_ptr(),
-          S.data_ptr(), o.data_ptr(), _handle(stream, dev))
+          S.data_ptr(), o.data_ptr(), clear, _handle(stream, dev))
     return o
 
 

@@ -1007,7 +1007,7 @@ static kda_status_t check_tree_sizes(int N, int H, int T, kda_dtype_t dtype) {
 
 kda_status_t kda_decode_tree(int N, int H, int T, kda_dtype_t dtype, const void* q, const void* k,
                              const void* v, const float* log_g, const void* beta,
-                             const int32_t* parents, const float* S, void* o,
+                             const int32_t* parents, const float* S, void* o, int clear_absent,
                              kda_stream_t stream) {
     t_last_error[0] = 0;
     kda_status_t st = check_tree_sizes(N, H, T, dtype);
@@ -1029,7 +1029,7 @@ kda_status_t kda_decode_tree(int N, int H, int T, kda_dtype_t dtype, const void*
         KDA_OK)
         return st;
     kda::TreeParams p{q, k, v, log_g, beta, parents, const_cast<float*>(S), o, N, H, T, 0,
-                      dtype == KDA_BF16, nullptr};
+                      dtype == KDA_BF16, nullptr, clear_absent != 0};
     if ((st = device_error_word(&p.err)) != KDA_OK) return st;
     const cudaError_t e = kda::launch_decode_tree(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_decode_tree launch");
@@ -1055,7 +1055,7 @@ kda_status_t kda_commit_path(int N, int H, int T, int A, kda_dtype_t dtype, cons
         KDA_OK)
         return st;
     kda::TreeParams p{nullptr, k, v, log_g, beta, path, S_inout, nullptr, N, H, T, A,
-                      dtype == KDA_BF16, nullptr};
+                      dtype == KDA_BF16, nullptr, false};
     if ((st = device_error_word(&p.err)) != KDA_OK) return st;
     const cudaError_t e = kda::launch_commit_path(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_commit_path launch");

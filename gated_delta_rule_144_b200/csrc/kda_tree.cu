@@ -332,6 +332,8 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             set_device_error(p.err, DEV_BAD_INDEX);
             mbar_wait(bar, 0, kWaitCycles);
         }
+        for (int i = tid; p.clear && i < T * width; i += kThreads)
+            store_elem(static_cast<Tin*>(p.o), first + i / width * stride + c0 + i % width, 0.f);
         return;
     }
 
@@ -602,9 +604,12 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     Tin* o = static_cast<Tin*>(p.o) + first + y0 * stride + col;
     const unsigned long long bad = sm.bad[col];
 #pragma unroll
-    for (int i = 0; i < kY; ++i, o += stride)
+    for (int i = 0; i < kY; ++i, o += stride) {
         if (sm.par[y0 + i] != -2)
             store_elem(o, 0, bad >> (y0 + i) & 1 ? __int_as_float(0x7fc00000) : y[i]);
+        else if (p.clear && y0 + i < T)
+            store_elem(o, 0, 0.f);
+    }
 }
 
 // The commit. Two blocks per SM walk the (sequence, head) units: four warps work on one unit's state

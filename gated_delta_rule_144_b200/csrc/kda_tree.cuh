@@ -19,6 +19,7 @@ struct TreeParams {
     int N, H, T, A;
     bool bf16;
     unsigned* err;
+    bool clear;             // tree: zeros to the rows of o without a node
 };
 
 cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream);

@@ -399,18 +399,20 @@ kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_
  *   q, k, log_g : [N, T, H, 128] (q, k in dtype, log_g float32)   v, o : [N, T, H, 128] dtype
  *   beta        : [N, T, H] dtype
  *   parents     : int32 [N, T], device: -1 for a child of the committed state, else an earlier
- *                 node (0 <= parents[n, i] < i); -2 for no node (o keeps that row, and nothing of
- *                 it is read but its gate and key rows, whose values do not matter).
+ *                 node (0 <= parents[n, i] < i); -2 for no node (whatever its rows hold does not
+ *                 matter).
  *   S           : [N, H, 128, 128] float32.
+ *   clear_absent : 0: rows of o without a node stay as they are; else they become zero.
  * T <= KDA_TREE_MAX_NODES (KDA_ERR_UNSUPPORTED above). o must not overlap any other argument. A
- * sequence with other parents gets no outputs and sets KDA_ERR_BAD_INDEX in the device error word.
+ * sequence with other parents has no nodes and sets KDA_ERR_BAD_INDEX in the device error word.
  * The states meet bf16 rows in tf32 products (relative error 2^-11 per factor, below the output's
  * rounding), fp32 rows in split products (2^-21).
  */
 #define KDA_TREE_MAX_NODES 64
 kda_status_t kda_decode_tree(int N, int H, int T, kda_dtype_t dtype, const void* q, const void* k,
                              const void* v, const float* log_g, const void* beta,
-                             const int32_t* parents, const float* S, void* o, kda_stream_t stream);
+                             const int32_t* parents, const float* S, void* o, int clear_absent,
+                             kda_stream_t stream);
 
 /*
  * kda_commit_path - advance N sequences' states in place by the rows that a path names: what

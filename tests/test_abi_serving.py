@@ -84,7 +84,7 @@ def test_linear_decode_refuses(L):
 def test_tree_and_path_refuse(L):
     def tree(N=1, H=2, T=4, dtype=1, q=far(0), par=far(6), o=far(5)):
         return L.kda_decode_tree(N, H, T, dtype, P(q), P(far(1)), P(far(2)), P(far(3)), P(far(4)),
-                                 P(par), P(far(7)), P(o), None)
+                                 P(par), P(far(7)), P(o), 0, None)
     assert tree(N=-1) == INVALID and tree(H=0) == INVALID and tree(dtype=2) == INVALID
     assert tree(T=65) == UNSUPPORTED and tree(q=None) == INVALID and tree(par=far(6) + 4) == INVALID
     assert tree(o=far(0)) == INVALID and tree(o=far(7) + 65536) == INVALID

@@ -96,6 +96,29 @@ def test_tree(N, T, H, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,T,H", [(3, 5, 2), (3, 40, 1), (40, 18, 4)])
+def test_tree_without_nodes(N, T, H, dtype):
+    """Absent nodes and rejected sequences: zeros in a new output, untouched rows in a given one."""
+    x = make(N, T, H, dtype, seed=31)
+    parents = random_parents(N, T, 32, "holes")
+    parents[-1] = 0                                     # rejected: node 0 its own parent
+    parents[1, :] = -2
+    p = torch.tensor(parents, device=DEV)
+    given = torch.full_like(x["q"], 7.0)
+    kda.decode_tree(x["q"], x["k"], x["v"], x["log_g"], x["beta"], p, x["S"], o=given)
+    assert kda.get_device_error() == 7
+    poison = torch.full_like(given, float("nan"))       # what a new output is likely to find there
+    torch.cuda.synchronize()
+    del poison
+    o = kda.decode_tree(x["q"], x["k"], x["v"], x["log_g"], x["beta"], p, x["S"])
+    assert kda.get_device_error() == 7
+    there = p != -2
+    there[-1] = False
+    assert torch.equal(o[there], given[there])
+    assert not o[~there].any() and (given[~there] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_steep_gates(dtype):
     x = make(2, 20, 2, dtype, seed=1)
     x["log_g"][0, 3] = -float("inf")
