@@ -43,8 +43,9 @@ constexpr int kD = 128;
 // Threads of a tree's block: one per value column and block of nodes in the solve, 8 warps at least.
 constexpr int tree_threads(int nb) { return nb > 2 ? 512 : 256; }
 constexpr int kB = 16;       // nodes per block of the solve
-constexpr int kLd = 136;     // floats per row of the products
-constexpr int kLk = 132;     // floats per row of k: eight rows' fragments in different banks
+// Floats per row, so that a fragment's rows fall in different banks: of the products (16 apart: two
+// rows of 16 columns), of k (8 apart: four rows of 8), and between nodes of the pairs.
+constexpr int kLd = kD + 16, kLk = kD + 8, kPad = 4;
 constexpr float kSteep = 1e-20f;   // a path product below this, or a quotient above the other,
 constexpr float kLarge = 1e30f;    // takes the direct walk
 constexpr uint32_t kStateBytes = kD * kD * 4;
@@ -106,28 +107,27 @@ __device__ __forceinline__ float warp_sum8(const float (&x)[8], int lane) {
 }
 
 // Row r (of 16) of a tile of the left operand, channels 4 lane .. 4 lane + 3, into fragment order:
-// per 8 channels 128 floats, lane 4 g + t's four values (rows g, g + 8, channels t, t + 4) together,
-// the lanes' places permuted by the channel block so that the blocks' stores fall in different
-// banks.
+// per 8 channels 128 floats, lane 4 g + t's four values (rows g, g + 8, channels 2 t, 2 t + 1)
+// together, the lanes' places permuted by the channel block so that the blocks' stores fall in
+// different banks. (A product's step sums over 8 channels in any order; with these pairs the rows of
+// S that four lanes read are 0, 2, 4, 6, whose swizzled pieces are in different banks.)
 template <bool kRound>   // to tf32, for the plain product
 __device__ __forceinline__ void store_frag(float* tile, int r, int lane, float4 x) {
     if (kRound)
         x = make_float4(__uint_as_float(tf32_rn(x.x)), __uint_as_float(tf32_rn(x.y)),
                         __uint_as_float(tf32_rn(x.z)), __uint_as_float(tf32_rn(x.w)));
-    const int ks = lane >> 1, sw = ks & 7;
-    float* p = tile + ks * 128 + (r >> 3) + 2 * (lane & 1);
-    const int l0 = (r & 7) * 4;
-    p[4 * ((l0 + 0) ^ sw)] = x.x;
-    p[4 * ((l0 + 1) ^ sw)] = x.y;
-    p[4 * ((l0 + 2) ^ sw)] = x.z;
-    p[4 * ((l0 + 3) ^ sw)] = x.w;
+    const int ks = lane >> 1, l0 = (r & 7) * 4 + 2 * (lane & 1);
+    float* p = tile + ks * 128 + 2 * (r >> 3);
+    *reinterpret_cast<float2*>(p + 4 * (l0 ^ (ks & 7))) = make_float2(x.x, x.y);
+    *reinterpret_cast<float2*>(p + 4 * ((l0 + 1) ^ (ks & 7))) = make_float2(x.z, x.w);
 }
 __device__ __forceinline__ float4 load_frag(const float* tile, int ks, int lane) {
-    return load4(tile + ks * 128 + 4 * (lane ^ (ks & 7)));
+    const float4 x = load4(tile + ks * 128 + 4 * (lane ^ (ks & 7)));
+    return make_float4(x.x, x.z, x.y, x.w);   // (rows g, g + 8 of the first channel, of the second)
 }
 
-// acc += one 16-row tile (fragments a) times 16 columns of the state (this lane's rows t and
-// t + 4 of 8, columns 2 g and 2 g + 1: one per 8-column product).
+// acc += one 16-row tile (fragments a) times 16 columns of the state (this lane's rows 2 t and
+// 2 t + 1 of 8, columns 2 g and 2 g + 1: one per 8-column product).
 // Without kSplit the fragments are tf32 values already, and the state's low bits, which the
 // product does not read, are cut off (2^-10 of an element at most).
 template <bool kSplit>
@@ -201,7 +201,8 @@ struct TreeSmem {
     // the gates, then path products; then the left operand; then u, [node][column]
     float frag[2 * kN * kD];
     float k[kN * kLk];                   // k, then k / (path product)
-    float akk[kN * kN], aqk[kN * kN];    // [j][i]: pairs of node i and j above it (and j = i)
+    static constexpr int kP = kN + kPad;
+    float akk[kN * kP], aqk[kN * kP];    // [j][i]: pairs of node i and j above it (and j = i)
     unsigned long long bad[kD];          // by column: nodes whose u is infinite or NaN
     unsigned long long above[kN];        // the nodes above each node
     alignas(16) int par[kN];
@@ -215,8 +216,9 @@ struct TreeSmem {
 template <typename Tin, int NB>
 __device__ __noinline__ void direct_pairs(TreeSmem<Tin, NB>& sm, const TreeParams& p, int n, int h,
                                           int warp, int lane) {
+    using Smem = TreeSmem<Tin, NB>;
     constexpr int kN = kB * NB, kWarps = tree_threads(NB) / 32;
-    for (int i = (int)threadIdx.x; i < kN * kN / 2; i += 32 * kWarps)   // both matrices
+    for (int i = (int)threadIdx.x; i < kN * Smem::kP / 2; i += 32 * kWarps)   // both matrices
         *reinterpret_cast<float4*>(sm.akk + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
     const Tin* q = static_cast<const Tin*>(p.q);
@@ -229,8 +231,8 @@ __device__ __noinline__ void direct_pairs(TreeSmem<Tin, NB>& sm, const TreeParam
             const float4 kj = mul4(d, load4(sm.k + j * kLk + 4 * lane));
             const float x[8] = {dot4(ki, kj), dot4(qi, kj), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const float sum = warp_sum8(x, lane);
-            if (lane == 0 && j != i) sm.akk[j * kN + i] = sum;
-            if (lane == 4) sm.aqk[j * kN + i] = sum;
+            if (lane == 0 && j != i) sm.akk[j * Smem::kP + i] = sum;
+            if (lane == 4) sm.aqk[j * Smem::kP + i] = sum;
             const float4 g = load4(p.log_g + at(j));
             d = mul4(d, make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w)));
         }
@@ -241,7 +243,7 @@ template <typename Tin, int NB>
 __global__ void __launch_bounds__(tree_threads(NB), NB == 1 && sizeof(Tin) == 2 ? 2 : 1)
 decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
     using Smem = TreeSmem<Tin, NB>;
-    constexpr int kN = Smem::kN, kThreads = tree_threads(NB), kWarps = kThreads / 32;
+    constexpr int kN = Smem::kN, kP = Smem::kP, kThreads = tree_threads(NB), kWarps = kThreads / 32;
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -440,8 +442,8 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
         int at0[kN8], at1[kN8];
 #pragma unroll
         for (int e = 0; e < kN8; ++e) {
-            at0[e] = state_at(lane & 3, cols + 16 * e + 2 * (lane >> 2));
-            at1[e] = state_at((lane & 3) + 4, cols + 16 * e + 2 * (lane >> 2));
+            at0[e] = state_at(2 * (lane & 3), cols + 16 * e + 2 * (lane >> 2));
+            at1[e] = state_at(2 * (lane & 3) + 1, cols + 16 * e + 2 * (lane >> 2));
         }
         float a0[2 * NB][kN8][4], a1[2 * NB][kN8][4];
 #pragma unroll
@@ -488,19 +490,20 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             int nt = tile % kTiles, blk = 0;
             while (nt >= 2 * (blk + 1)) nt -= 2 * ++blk;
             float c[2][4] = {};   // sums of even and odd steps
-            const float* b = sm.k + (8 * nt + (lane >> 2)) * kLk + (lane & 3);
+            const float* b = sm.k + (8 * nt + (lane >> 2)) * kLk + 2 * (lane & 3);
             const float* a = sm.frag + (half * NB + blk) * 2048;
 #pragma unroll 8
-            for (int ks = 0; ks < 16; ++ks)
-                mma_step<sizeof(Tin) == 4>(c[ks & 1], load_frag(a, ks, lane), b[8 * ks],
-                                           b[8 * ks + 4]);
+            for (int ks = 0; ks < 16; ++ks) {
+                const float2 y = *reinterpret_cast<const float2*>(b + 8 * ks);
+                mma_step<sizeof(Tin) == 4>(c[ks & 1], load_frag(a, ks, lane), y.x, y.y);
+            }
             float* to = half ? sm.aqk : sm.akk;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {   // rows g, g + 8; nodes 2 t, 2 t + 1
                 const int i = 16 * blk + (lane >> 2) + 8 * (e >> 1);
                 const int j = 8 * nt + 2 * (lane & 3) + (e & 1);
                 const bool pair = (s_above[i] >> j & 1) || (half && i == j);
-                to[j * kN + i] = pair ? c[0][e] + c[1][e] : 0.f;
+                to[j * kP + i] = pair ? c[0][e] + c[1][e] : 0.f;
             }
         }
     }
@@ -518,7 +521,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     }
     // r less what node `at`'s u adds to the rows e of block `to`, first <= e
     auto spread = [&](int at, int to, float u, int first) {
-        const float* ak = sm.akk + at * kN + kB * to;
+        const float* ak = sm.akk + at * kP + kB * to;
 #pragma unroll
         for (int i4 = 0; i4 < kB; i4 += 4) {
             if (i4 + 3 < first) continue;
@@ -538,13 +541,13 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
         for (int i = 0; i < kY; ++i) y[i] = sm.state[(kN + y0 + i) * kLd + col];
     }
     auto read_out = [&](int b) {
-        const float *u = s_u + kB * b * kD + col, *aq = sm.aqk + kB * b * kN + y0;
+        const float *u = s_u + kB * b * kD + col, *aq = sm.aqk + kB * b * kP + y0;
 #pragma unroll 4
         for (int j = 0; j < kB; ++j) {
             const float x = u[j * kD];
 #pragma unroll
             for (int i = 0; i < kY; i += 4) {
-                const float4 c = load4(aq + j * kN + i);
+                const float4 c = load4(aq + j * kP + i);
                 y[i] = fmaf(c.x, x, y[i]), y[i + 1] = fmaf(c.y, x, y[i + 1]);
                 y[i + 2] = fmaf(c.z, x, y[i + 2]), y[i + 3] = fmaf(c.w, x, y[i + 3]);
             }
@@ -577,7 +580,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 #pragma unroll 1
                 for (int j = 0; j < kB; ++j) {
                     const int at = kB * b + j;
-                    const float* ak = sm.akk + at * kN + kB * b;
+                    const float* ak = sm.akk + at * kP + kB * b;
                     float u = sm.beta[at] * rs[j * kLd];
                     if (bad & s_above[at] || !(fabsf(u) <= 3.402823466e38f)) {
                         u = 0.f;
