@@ -15,10 +15,10 @@
 //     The products of the first and of the two small terms are summed apart and meet in fp32.
 //   - q S reads the state rounded to bf16, and the decayed scores are rounded to bf16: each 2^-9
 //     of a term at most, as the output's own rounding, on disjoint parts of the output.
-//   - Gate sums are held in powers of two. Decays are products of gates <= 1: a pair of rows in different 32-row blocks takes
-//     (suffix of j's block) (blocks between) (prefix of i's block), so no exponential grows
-//     and none is taken of a difference of large sums; inside a block G_i - G_j is a
-//     difference of sums over at most 32 rows. Gates below -110 count as -110, whose
+//   - Gate sums are held in powers of two. Decays are products of gates <= 1: a pair of rows in
+//     different 32-row blocks takes (suffix of j's block) (blocks between) (prefix of i's block),
+//     so no exponential grows and none is taken of a difference of large sums; inside a block
+//     G_i - G_j is a difference of sums over at most 32 rows. Gates below -110 count as -110, whose
 //     exponential is 0 in fp32 like that of anything below.
 //
 // Roles (16 warps), which meet through mbarriers only:
@@ -39,8 +39,16 @@
 // chunk, all at the same time, and the kernel is bound by instruction fetch where their sum
 // outgrows the cache (132 KB of code ran a chunk in 7.2 us, the same loops rolled up, 77 KB, in
 // 3.3 us).
-// TMEM: P 128 columns, bf16 P 64, P V 64, Q S 2 x 64, the state's terms 2 x 64: all 512. Shared memory:
-// 2 x 80 KiB of stages, 24 KiB of decayed V, 16 KiB of bf16 state, 16 KiB of output.
+// Bound: shared memory. A chunk of a CTA takes about 3690 cycles, of which about 3375 move operands,
+// decayed V, state and output through it. 2 x 65536 tokens x 32 heads x 128 x 128 take 1.08 to 1.16
+// ms in a burst (0.58 of the measured copy rate) and 1.31 to 1.36 in a long run, where the power
+// limit holds the clock down; eight packed documents of 28937 tokens, 32 heads of 64 columns 160 to
+// 170 us; one prompt of 4096 tokens x 16 heads 47 us. Not kept, on the first of these: tiles fetched
+// into L2 two chunks ahead 1.15 (against 1.10), one product of 192 columns for all terms 1.36
+// (1.15), the last quarter of the values by the state warps 1.30 (1.15), outputs stored by each warp
+// for itself 1.23 (1.14).
+// TMEM: P 128 columns, bf16 P 64, P V 64, Q S 2 x 64, the state's terms 2 x 64: all 512. Shared
+// memory: 2 x 80 KiB of stages, 24 KiB of decayed V, 16 KiB of bf16 state, 16 KiB of output.
 // Every wait is bounded; on expiry the CTA records KDA_ERR_TIMEOUT, drains its copies and
 // products, frees TMEM and exits.
 

@@ -25,8 +25,15 @@
 //            remainder and sum three products (2^-21).
 //   solve    a thread per value column and block of 16 nodes substitutes forward in registers:
 //            each u, once known, leaves all later rows' sums, so that a step waits for one
-//            product only; then the blocks behind take the block's u from shared memory.
-// Bound: HBM (64 KiB of state per block, twice for the commit).
+//            product only; then the blocks behind take the block's u from shared memory, and the
+//            threads that wait add it to their read-outs.
+// Bound: the phases' latency, two blocks per SM beside each other; HBM (64 KiB of state per block) in
+// the limit. 128 sequences x 32 heads, 16 bf16 nodes: 105 us (0.54 of the measured copy rate), a
+// block's cycles 3400 until rows and gates are there, 950 paths, 1100 quotients and fragments, 3900
+// products (a tf32 product takes 18 to 20 cycles of a scheduler), 1300 solve, 2200 read-outs. One
+// sequence of 61 nodes and 32 heads: 16.9 us in a graph (20.3 with one block per unit). Before: read-outs
+// within the substitution and v loaded by the solve's threads 136 and 26.6 us; path products in
+// rounds that double the stretch covered 125 and 22.
 
 #include <algorithm>
 
@@ -261,8 +268,9 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     const int col = tid & (kD - 1), blk = tid >> 7;   // the solve's column and group of nodes
     const bool mine = col >= c0 && col < c0 + width;
     float4 qd[kMine], kd[kMine];
-    // half of the warps take the products with S, kCols columns each, whose sums for the rows k d
-    // start from -v
+    // half of the warps take the products with S, kCols columns each, and take v from the sums of
+    // the rows k d: bf16 rows before the products, whose accumulation cuts sums off at 2^-23 of their
+    // size, fp32 rows after them
     constexpr int kCols = kD / (kWarps / 2), kN8 = kCols / 16;   // columns, pairs of 8 of them
     const int cols = kCols * warp;
     const bool own = cols >= c0 && cols < c0 + width;
@@ -451,12 +459,20 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 #pragma unroll
             for (int e = 0; e < kN8; ++e)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {   // (a tile's four columns as store_tile has them)
-                    const float4 y = b < NB ? widen(vr[b < NB ? b : 0][e][x])
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                    a0[b][e][2 * x] = -y.x, a1[b][e][2 * x] = -y.y;
-                    a0[b][e][2 * x + 1] = -y.z, a1[b][e][2 * x + 1] = -y.w;
-                }
+                for (int x = 0; x < 4; ++x) a0[b][e][x] = a1[b][e][x] = 0.f;
+        auto less_v = [&] {   // (a tile's four columns as store_tile has them)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < kN8; ++e)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float4 y = widen(vr[b][e][x]);
+                        a0[b][e][2 * x] -= y.x, a1[b][e][2 * x] -= y.y;
+                        a0[b][e][2 * x + 1] -= y.z, a1[b][e][2 * x + 1] -= y.w;
+                    }
+        };
+        if (sizeof(Tin) == 2) less_v();
 #pragma unroll 2
         for (int ks = 0; ks < 16; ++ks) {
             float2 s0[kN8], s1[kN8];
@@ -473,6 +489,7 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
                     mma_step<sizeof(Tin) == 4>(a0[b][e], a1[b][e], f, s0[e], s1[e]);
             }
         }
+        if (sizeof(Tin) == 4) less_v();
         bar_sync(1, 32 * width / kCols);   // S has been read
 #pragma unroll
         for (int b = 0; b < 2 * NB; ++b)
@@ -621,7 +638,9 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 // gates are its own running products), then, as (row phase, four columns), 32 rows of the state:
 // k d S, the substitution for u in registers, and S = d_e S + sum_j (d_ej k_j) u_j^T, each one pass
 // over the registers. (Tensor-core products of 16-row tiles, split for fp32, take more instructions
-// up to about 9 rows.)
+// up to about 9 rows: 567 us against 280 then.) Bound: HBM (the state read and written). 256
+// sequences x 32 heads, paths of up to 6 of 16 bf16 rows: 210 to 215 us, 0.80 of the measured copy
+// rate; 280 without the loader warp.
 constexpr int kRows = 4;
 constexpr int kPathWorkers = 128, kPathThreads = kPathWorkers + 32;
 template <typename Tin>
@@ -885,6 +904,8 @@ cudaError_t launch_tree(const TreeParams& p, int sms, cudaStream_t stream) {
                                       (unsigned long long)p.N * p.H * kD, kD, 32, kD,
                                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
+    // two blocks per unit, half of the value columns each, where SMs are to spare (32 units, 61 nodes:
+    // 16.9 us against 20.3 with one, 30 nodes 9.95 / 10.4, 12 nodes 6.06 / 6.43)
     const dim3 grid((unsigned)(p.N * p.H), p.N * p.H * 2 <= sms ? 2 : 1);
     decode_tree_kernel<Tin, NB>
         <<<grid, tree_threads(NB), sizeof(TreeSmem<Tin, NB>), stream>>>(map, p);

@@ -95,6 +95,26 @@ def test_tree(N, T, H, kind, dtype):
     check_tree(x, parents, o, before)
 
 
+@pytest.mark.parametrize("T", [1, 5, 16, 30, 61])
+def test_tree_keeps_fp32(T):
+    """fp32 rows, 1.3e-6: a tensor-core accumulation cuts a sum off at 2^-23 of its size, half of that
+    on average, and running sums are about two thirds of the last one. A pair's coefficient is two
+    sums of 24 steps: 24 x 2^-24 x 2/3 = 9.5e-7 of the output. The products with S take 48 steps,
+    1.9e-6 of a part that is a tenth of the output here (S is scaled down); v must not pass
+    through those sums. The split factors leave 2^-22 of the same terms."""
+    x = make(3, T, 2, "f32", seed=77)
+    x["S"] *= 0.1
+    parents = random_parents(3, T, 78)
+    o = kda.decode_tree(x["q"], x["k"], x["v"], x["log_g"], x["beta"],
+                        torch.tensor(parents, device=DEV), x["S"])
+    assert kda.get_device_error() == 0
+    there = parents != -2
+    ref = np.zeros(tuple(o.shape))
+    for n, i in np.argwhere(there):
+        ref[n, i] = walk(x, n, path_of(parents[n], i))[0][0, -1]
+    assert rel_l2(host(o)[there], ref[there]) <= 1.3e-6
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,T,H", [(3, 5, 2), (3, 40, 1), (40, 18, 4)])
 def test_tree_without_nodes(N, T, H, dtype):
