@@ -642,12 +642,13 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 // sequences x 32 heads, paths of up to 6 of 16 bf16 rows: 210 to 215 us, 0.80 of the measured copy
 // rate; 280 without the loader warp.
 constexpr int kRows = 4;
+constexpr int kStaged = 8;   // rows of a path that the loader brings
 constexpr int kPathWorkers = 128, kPathThreads = kPathWorkers + 32;
 template <typename Tin>
 struct PathSmem {
     float state[kD * kD];           // the next unit's state
-    Tin k[2][kRows][kD], v[2][kRows][kD];   // first rows of this unit and the next
-    float g[2][kRows][kD], beta[2][kRows];
+    Tin k[2][kStaged][kD], v[2][kStaged][kD];   // first rows of this unit and the next
+    float g[2][kStaged][kD], beta[2][kStaged];
     float4 kd[kD], ke[kD];          // [channel][row]: k_j d_j, d_ej k_j
     float end[kD];                  // d_e
     float pairs[4][8];              // per warp: pair sums
@@ -700,7 +701,7 @@ commit_path_kernel(const TreeParams p, const int units) {
             if (len == 0) continue;
             // the workers have the previous state in registers, and are done with this buffer's
             // rows
-            const int b = it & 1, m = min(len, kRows);
+            const int b = it & 1, m = min(len, kStaged);
             if (it > 0) ok = __all_sync(0xffffffffu, mbar_wait(free, (it - 1) & 1, kWaitCycles));
             if (!ok) {   // (nothing of this CTA is in flight)
                 if (lane == 0) {
@@ -710,7 +711,7 @@ commit_path_kernel(const TreeParams p, const int units) {
                 break;
             }
             const uint32_t bar = full + 8 * b;
-            if (lane < kRows)
+            if (lane < kStaged)
                 sm.beta[b][lane] = lane < m ? load_elem(static_cast<const Tin*>(p.beta),
                                                         ((int64_t)n * p.T + first) * p.H + h)
                                             : 0.f;
@@ -782,9 +783,9 @@ commit_path_kernel(const TreeParams p, const int units) {
                 kk[j] = 0.f;
                 gg[j] = 1.f;
                 if (a0 + j >= len) continue;
-                if (a0 == 0) {
-                    kk[j] = load_elem(sm.k[b][j], tid);
-                    gg[j] = expf(sm.g[b][j][tid]);
+                if (a0 < kStaged) {
+                    kk[j] = load_elem(sm.k[b][a0 + j], tid);
+                    gg[j] = expf(sm.g[b][a0 + j][tid]);
                 } else {
                     const size_t at = row(a0 + j) + tid;
                     kk[j] = load_elem(k, at);
@@ -833,7 +834,8 @@ commit_path_kernel(const TreeParams p, const int units) {
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
                 float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (a0 + j < len) r = a0 == 0 ? load4(sm.v[b][j] + col) : load4(v + row(a0 + j) + col);
+                if (a0 + j < len)
+                    r = a0 < kStaged ? load4(sm.v[b][a0 + j] + col) : load4(v + row(a0 + j) + col);
                 r = make_float4(r.x - y[j].x, r.y - y[j].y, r.z - y[j].z, r.w - y[j].w);
 #pragma unroll
                 for (int l = 0; l < j; ++l) {
@@ -844,7 +846,7 @@ commit_path_kernel(const TreeParams p, const int units) {
                     r.z = fmaf(a, y[l].z, r.z), r.w = fmaf(a, y[l].w, r.w);
                 }
                 const float beta =
-                    a0 == 0 ? sm.beta[b][j]
+                    a0 < kStaged ? sm.beta[b][a0 + j]
                     : a0 + j < len ? load_elem(static_cast<const Tin*>(p.beta), row(a0 + j) / kD)
                                    : 0.f;
                 y[j] = make_float4(beta * r.x, beta * r.y, beta * r.z, beta * r.w);
