@@ -570,7 +570,7 @@ def _empty(like, shape, dtype, stream):
     pending on the current stream still uses it and its reuse follows the call."""
     if stream is None:
         return (torch.empty_like(like) if shape is None
-                else torch.empty(shape, dtype=dtype, device=like.device))
+                else like.new_empty(shape, dtype=dtype))
     with torch.cuda.stream(stream):
         return _empty(like, shape, dtype, None)
 

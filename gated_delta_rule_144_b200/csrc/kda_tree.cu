@@ -639,8 +639,9 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 // k d S, the substitution for u in registers, and S = d_e S + sum_j (d_ej k_j) u_j^T, each one pass
 // over the registers. (Tensor-core products of 16-row tiles, split for fp32, take more instructions
 // up to about 9 rows: 567 us against 280 then.) Bound: HBM (the state read and written). 256
-// sequences x 32 heads, paths of up to 6 of 16 bf16 rows: 210 to 215 us, 0.80 of the measured copy
-// rate; 280 without the loader warp.
+// sequences x 32 heads, paths of up to 6 of 16 bf16 rows: 192 us, 0.89 of the measured copy
+// rate; 211 with only four rows brought ahead, 280 without the loader warp; 199 with a path's last
+// one or two rows taken as two instead of four.
 constexpr int kRows = 4;
 constexpr int kStaged = 8;   // rows of a path that the loader brings
 constexpr int kPathWorkers = 128, kPathThreads = kPathWorkers + 32;
