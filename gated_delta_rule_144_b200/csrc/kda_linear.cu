@@ -256,7 +256,7 @@ linear_combine_kernel(const LinearParams p) {
     } else {
         first = (long long)n * max(1, (p.T + L - 1) / L);
     }
-    const int segs = (int)((len + L - 1) / L);
+    const int segs = len <= p.whole_tokens ? 1 : (int)((len + L - 1) / L);
     if (segs < 2 || e >= unit) return;
     float S = p.h0 ? p.h0[((size_t)n * p.H + h) * unit + e] : 0.f;
     float* st = p.seg_state + ((size_t)first * p.H + h) * unit + e;

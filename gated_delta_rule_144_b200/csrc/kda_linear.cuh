@@ -28,6 +28,7 @@ struct LinearParams {
     // equal-length sequences, else floor(cu[n] / seg_tokens) + n + s (strictly increasing over
     // (n, s), so slots never collide and g < slots = floor(T / seg_tokens) + N)
     int seg_tokens;
+    int whole_tokens;           // packed, chunked: sequences up to this long are one segment
     int slots;                  // slots per head (N without segments)
     float* seg_state;           // [slots, H, dk, dv]: B, then the segment's initial state
     float* seg_decay;           // [slots, H]

@@ -42,8 +42,8 @@
 // Bound: shared memory. A chunk of a CTA takes about 3690 cycles, of which about 3375 move operands,
 // decayed V, state and output through it. 2 x 65536 tokens x 32 heads x 128 x 128 take 1.08 to 1.16
 // ms in a burst (0.58 of the measured copy rate) and 1.31 to 1.36 in a long run, where the power
-// limit holds the clock down; eight packed documents of 28937 tokens, 32 heads of 64 columns 160 to
-// 170 us; one prompt of 4096 tokens x 16 heads 47 us. Not kept, on the first of these: tiles fetched
+// limit holds the clock down; eight packed documents of 28937 tokens, 32 heads of 64 columns 156 to
+// 165 us; one prompt of 4096 tokens x 16 heads 47 us. Not kept, on the first of these: tiles fetched
 // into L2 two chunks ahead 1.15 (against 1.10), one product of 192 columns for all terms 1.36
 // (1.15), the last quarter of the values by the state warps 1.30 (1.15), outputs stored by each warp
 // for itself 1.23 (1.14).
@@ -169,11 +169,12 @@ constexpr int kSorted = 128;    // packed slots up to which CTAs take them longe
                                 // all of them: 32 comparisons per thread)
 constexpr int kScanned = 1024;  // packed sequences up to which every CTA reads all offsets
 
-// The CTA's g-th slot, found by the whole block; `tmp` is kSorted ints of shared memory. Equal
-// lengths: first segments first (they wait for nothing). Packed: longest first up to kSorted
+// The CTA's g-th slot, found by the whole block (kStates: the g-th segment that is not its sequence's
+// last); `tmp` is kSorted ints of shared memory. Equal lengths: first segments first (they wait for nothing). Packed: longest first up to kSorted
 // slots, so that no long one starts last. Every CTA reads all offsets, and a malformed cu_seqlens
 // makes each of them report it and stop; above kScanned sequences, which are never cut into
 // segments, each checks its own, and some CTA meets what is malformed. False: nothing to do.
+template <bool kStates>
 __device__ __forceinline__ bool chunk_slot(const LinearParams& p, int g, int tid, int* tmp,
                                            ChunkSlot* s) {
     const int L = p.seg_tokens;
@@ -211,8 +212,43 @@ __device__ __forceinline__ bool chunk_slot(const LinearParams& p, int g, int tid
     auto first = [&](int n) { return L > 0 ? cu[n] / L + n : n; };
     auto rows = [&](int n, int slot) {
         const int len = cu[n + 1] - cu[n], at = L > 0 ? (slot - first(n)) * L : 0;
-        return at == 0 ? (L > 0 ? min(len, L) : len) : at < len ? min(len - at, L) : -1;
+        if (L <= 0 || len <= p.whole_tokens) return at == 0 ? len : -1;
+        return at < len ? min(len - at, L) : -1;
     };
+    if (kStates) {   // counts of such segments, summed over the sequences before each
+        const int lane = tid & 31, warp = tid >> 5;
+        int base = 0;
+        for (int i0 = 0; i0 < p.N; i0 += kThreads) {
+            const int n = i0 + tid, len = n < p.N ? cu[n + 1] - cu[n] : 0;
+            const int mine = len <= p.whole_tokens ? 0 : (len - 1) / L;
+            int sum = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, off);
+                if (lane >= off) sum += x;
+            }
+            if (lane == 31) tmp[warp] = sum;
+            __syncthreads();
+            int all = 0, before = base;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                before += w < warp ? tmp[w] : 0;
+                all += tmp[w];
+            }
+            before += sum - mine;
+            if (g >= before && g < before + mine)
+                tmp[kThreads / 32] = n, tmp[kThreads / 32 + 1] = g - before;
+            base += all;
+            __syncthreads();
+        }
+        if (g >= base) return false;
+        s->n = tmp[kThreads / 32];
+        s->seg = tmp[kThreads / 32 + 1];
+        s->slot = first(s->n) + s->seg;
+        s->begin = cu[s->n] + (long long)s->seg * L;
+        s->end = s->begin + L;
+        s->last = false;
+        return true;
+    }
     int slot = g;
     if (p.slots <= kSorted) {
         for (int i = tid; i < p.slots; i += kThreads) tmp[i] = -1;   // (slots that nothing uses)
@@ -354,10 +390,9 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     const int h = blockIdx.x / args.tiles % p.H, g = blockIdx.x / args.tiles / p.H;
     const int hk = h / (p.H / p.Hk);
     ChunkSlot sl;
-    if (!chunk_slot(p, g, tid, reinterpret_cast<int*>(sm), &sl)) return;
+    if (!chunk_slot<!kOut>(p, g, tid, reinterpret_cast<int*>(sm), &sl)) return;
     // the outputs' launch may start now; what it reads of this one it waits for
     if (!kOut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!kOut && sl.last) return;
     const int nchunks = (int)((sl.end - sl.begin + kC - 1) / kC);
     const int j0 = tile * kNV;
     constexpr int kBufs = kOut ? 2 : 4;
@@ -909,7 +944,9 @@ cudaError_t launch_linear_chunk(const LinearParams& p, LinearPass pass, cudaStre
     });
     if (e != cudaSuccess) return e;
     ChunkArgs a{p, (p.dv + kNV - 1) / kNV, wait_budget(), debug_stall()};
-    const long long blocks = (long long)p.slots * p.H * a.tiles;
+    // (there are at most slots - N segments that are not a sequence's last)
+    const long long slots = pass == LinearPass::kStates ? p.slots - p.N : p.slots;
+    const long long blocks = slots * p.H * a.tiles;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
     ChunkMaps m;

@@ -282,7 +282,8 @@ def test_long_prompt_single_head(T):
 
 
 @pytest.mark.parametrize("lens", [[3000, 1, 0, 500], [100] * 40, [1] * 1100, [2000, 0, 3, 2500, 700],
-                                  [0, 0, 5000]], ids=lambda x: "%dx%d" % (len(x), max(x)))
+                                  [0, 0, 5000], [1632, 1633, 0, 1025, 1, 1024, 2048, 2049, 3265],
+                                  [1633] * 5 + [700] * 600], ids=lambda x: "%dx%d" % (len(x), max(x)))
 def test_packed_few_heads(lens):
     """Documents longer than an SM's share are cut into segments; very many are taken in order."""
     x = make(1, sum(lens), 1, 1, 32, 64, N=len(lens), seed=len(lens))
