@@ -170,10 +170,11 @@ constexpr int kSorted = 128;    // packed slots up to which CTAs take them longe
 constexpr int kScanned = 1024;  // packed sequences up to which every CTA reads all offsets
 
 // The CTA's g-th slot, found by the whole block (kStates: the g-th segment that is not its sequence's
-// last); `tmp` is kSorted ints of shared memory. Equal lengths: first segments first (they wait for nothing). Packed: longest first up to kSorted
-// slots, so that no long one starts last. Every CTA reads all offsets, and a malformed cu_seqlens
-// makes each of them report it and stop; above kScanned sequences, which are never cut into
-// segments, each checks its own, and some CTA meets what is malformed. False: nothing to do.
+// last); `tmp` is kSorted ints of shared memory. Equal lengths: first segments first (they wait for
+// nothing). Packed: longest first up to kSorted slots, so that no long one starts last. Every CTA
+// reads all offsets, and a malformed cu_seqlens makes each of them report it and stop; above
+// kScanned sequences, which are never cut into segments, each checks its own, and some CTA meets
+// what is malformed. False: nothing to do.
 template <bool kStates>
 __device__ __forceinline__ bool chunk_slot(const LinearParams& p, int g, int tid, int* tmp,
                                            ChunkSlot* s) {
