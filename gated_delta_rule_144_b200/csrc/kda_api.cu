@@ -818,9 +818,10 @@ static bool linear_chunked(const kda_linear_desc_t* d) {
 
 // Tokens per segment of the per-token walk (0: whole sequences). The walk has one warp per 16 value
 // columns of a (segment, head) (8 above dk = 128); segments are cut so that about 4096 warps (7 per
-// scheduler) share the work: one fp32 prompt of 4096 tokens x 16 heads takes 357 us, 381 with 2048
-// warps. Below 64 tokens a segment's states cost more than it gains (4 x 1000 tokens x 4 heads 56
-// us at 64, 62 at 32), but for a short prompt (100 tokens x 16 heads: 52 us at 64, 41 at 32).
+// scheduler) share the work: one fp32 prompt of 4096 tokens x 16 heads takes 301 us, 346 with 2048
+// and 314 with 8192. Below 64 tokens a segment's states cost more than it gains (4 x 1000 tokens x 4
+// heads of 64 x 64 56 us at 64, 62 at 32), but for a short prompt (100 tokens x 16 heads: 52 us at
+// 64, 41 at 32 when it was chosen, 32 now).
 static int linear_walk_segment(const kda_linear_desc_t* d) {
     const int nc = d->dk <= 128 ? 16 : 8;
     const int64_t groups = (int64_t)d->H * ((d->dv + nc - 1) / nc);
