@@ -168,6 +168,23 @@ def test_bad_values_reach_no_earlier_token(T, spots, bad, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,t", [(300, 200), (300, 128), (700, 130), (9000, 5003)])
+@pytest.mark.parametrize("name", ["q", "k", "log_g"])
+def test_bad_rows_reach_no_earlier_token(name, T, t, dtype):
+    """A NaN in a row of q spoils that row's output, in k or a gate those from its token on."""
+    x = make(1, T, 2, 2, 128, 64, dtype, seed=8)
+    ro, _ = linear_attention(*(host(x[n]) for n in ("q", "k", "v", "log_g", "h0")))
+    x[name][(0, t, 1) + ((5,) if name != "log_g" else ())] = float("nan")
+    o, _ = kda.linear_fwd(**x)
+    assert kda.get_device_error() == 0
+    o = host(o)
+    clean = np.ones_like(o, dtype=bool)
+    clean[0, t:t + 1 if name == "q" else T, 1] = False
+    assert rel_l2(o[clean], ro[clean]) <= (TOL_BF16 if dtype == "bf16" else TOL_F32)
+    assert not np.isfinite(o[~clean]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,T,H,Hk,dk,dv", [(1, 1, 1, 1, 128, 128), (5, 1, 4, 2, 128, 64),
                                             (3, 4, 2, 2, 128, 128), (2, 9, 3, 1, 64, 128),
                                             (2, 1, 2, 2, 32, 96), (1, 3, 1, 1, 256, 256),

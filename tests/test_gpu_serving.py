@@ -165,3 +165,24 @@ def test_the_same_steps_captured_and_replayed():
         for name, pair in e.out.items():
             if name != "prompt":
                 assert all(torch.equal(a, b) for a, b in zip(pair, want[0][name])), name
+
+
+def test_two_engines_at_once():
+    """Two runs interleaved on two streams leave what each leaves by itself."""
+    alone = Engine()
+    alone.prefill()
+    alone.serve()
+    torch.cuda.synchronize()
+    streams, engines = [torch.cuda.Stream() for _ in range(2)], [Engine() for _ in range(2)]
+    torch.cuda.synchronize()
+    for step in ("prefill", "serve"):
+        for s, e in zip(streams, engines):
+            with torch.cuda.stream(s):
+                getattr(e, step)()
+    torch.cuda.synchronize()
+    assert kda.get_device_error() == 0
+    m = sum(LIVE)
+    for e in engines:
+        assert torch.equal(e.pool[:, :m], alone.pool[:, :m])
+        for name, pair in e.out.items():
+            assert all(torch.equal(a, b) for a, b in zip(pair, alone.out[name])), name
