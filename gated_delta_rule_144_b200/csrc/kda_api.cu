@@ -15,6 +15,7 @@
 #include "kda_bwd.cuh"
 #include "kda_internal.cuh"
 #include "kda_linear.cuh"
+#include "kda_pages.cuh"
 #include "kda_scan.cuh"
 #include "kda_tree.cuh"
 

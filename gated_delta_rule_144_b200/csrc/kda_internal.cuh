@@ -15,7 +15,6 @@ enum DeviceError : unsigned {
     DEV_TIMEOUT = 4,
     DEV_BAD_SEQLENS = 5,
     DEV_RANGE = 6,   // reserved: steep decays take the chunked kernels' direct path instead
-    DEV_BAD_INDEX = 7,
 };
 
 // The first error sticks; later ones are dropped.
@@ -127,10 +126,6 @@ cudaError_t launch_out_norm_gated(const void* x, const void* gate, const float* 
 cudaError_t launch_short_conv(const void* x, const float* w, const int32_t* cu, int N, void* y,
                               int B, int T, int C, int W, bool bf16, int act, int group, float eps,
                               unsigned* err, cudaStream_t stream);
-// Page dst[i] <- page src[i] (-1: zeros) of pool [layers][pages][page_bytes], i < n; dst[i] = -1
-// does nothing. Conflicting or out-of-range pairs are left out and set DEV_BAD_INDEX.
-cudaError_t launch_page_copy(void* pool, const int32_t* src, const int32_t* dst, int n, int layers,
-                             int pages, long long page_bytes, unsigned* err, cudaStream_t stream);
 bool chunk64_available();
 // Value columns one chunked-kernel CTA owns for N sequences x H heads (64 or 128).
 int chunk64_value_width(int N, int H);

@@ -11,7 +11,7 @@
 // 595 MB of moves and clears of 2 MiB pages take 96 us (0.95 of the measured copy rate), 8192 pairs of
 // 128 KiB 333 us (0.98); 20000 pairs of 16 KiB, where the list outweighs the page, 309 us (0.32).
 
-#include "kda_internal.cuh"
+#include "kda_pages.cuh"
 
 namespace kda {
 namespace {
