@@ -80,6 +80,9 @@ constexpr uint32_t OFF_SB = OFF_VH + 2 * kVH;       // bf16 state
 constexpr uint32_t OFF_OUT = OFF_SB + kPanel;       // output on its way to global memory
 constexpr uint32_t OFF_GATE = OFF_OUT + kPanel;      // per stage: loc[128], suf[128], tot[4]
 constexpr uint32_t kGateBytes = (2 * kC + 4) * 4;
+// A CTA's search for its slot runs in the gates' area, which plain stores alone write: a plain store
+// to a stage would need a proxy fence before the TMA copies there.
+constexpr uint32_t OFF_FIND = OFF_GATE;
 constexpr uint32_t OFF_BAR = OFF_GATE + 2 * kGateBytes;
 constexpr uint32_t OFF_MISC = OFF_BAR + 34 * 8;     // TMEM address, abort flag
 constexpr uint32_t kSmem = OFF_MISC + 16;
@@ -168,9 +171,12 @@ struct ChunkSlot {
 constexpr int kSorted = 128;    // packed slots up to which CTAs take them longest first (a CTA ranks
                                 // all of them: 32 comparisons per thread)
 constexpr int kScanned = 1024;  // packed sequences up to which every CTA reads all offsets
+constexpr int kFindInts = kSorted > kThreads / 32 + 2 ? kSorted : kThreads / 32 + 2;
+static_assert(OFF_FIND >= OFF_OUT + kPanel && OFF_FIND + 4 * kFindInts <= OFF_BAR,
+              "the search's words lie behind everything that TMA reads or writes");
 
 // The CTA's g-th slot, found by the whole block (kStates: the g-th segment that is not its sequence's
-// last); `tmp` is kSorted ints of shared memory. Equal lengths: first segments first (they wait for
+// last); `tmp` is kFindInts ints of shared memory. Equal lengths: first segments first (they wait for
 // nothing). Packed: longest first up to kSorted slots, so that no long one starts last. Every CTA
 // reads all offsets, and a malformed cu_seqlens makes each of them report it and stop; above
 // kScanned sequences, which are never cut into segments, each checks its own, and some CTA meets
@@ -391,7 +397,7 @@ linear_chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constan
     const int h = blockIdx.x / args.tiles % p.H, g = blockIdx.x / args.tiles / p.H;
     const int hk = h / (p.H / p.Hk);
     ChunkSlot sl;
-    if (!chunk_slot<!kOut>(p, g, tid, reinterpret_cast<int*>(sm), &sl)) return;
+    if (!chunk_slot<!kOut>(p, g, tid, reinterpret_cast<int*>(sm + OFF_FIND), &sl)) return;
     // the outputs' launch may start now; what it reads of this one it waits for
     if (!kOut) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int nchunks = (int)((sl.end - sl.begin + kC - 1) / kC);
