@@ -20,8 +20,9 @@
 //            included) the quotient leaves the range: then a warp per node walks the node's
 //            ancestors with d_ij in registers, where only products of gates <= 1 appear.
 //   product  [k d; q d] S on the tensor cores (warp-level tf32 products: 16 x 8 x 8). The tree of
-//            bf16 rows uses one tf32 product (its operands lose at most 2^-11 and 2^-10, below the
-//            bf16 output's 2^-8); fp32 rows split both operands into a tf32 part and a tf32
+//            bf16 rows uses one tf32 product (its operands, rounded to nearest, lose at most 2^-11
+//            each, below the bf16 output's 2^-8; with S and k / d cut off instead, 2^-10 and always
+//            towards zero, 128 sequences x 32 heads of 16 nodes take 2 us less); fp32 rows split both operands into a tf32 part and a tf32
 //            remainder and sum three products (2^-21).
 //   solve    a thread per value column and block of 16 nodes substitutes forward in registers:
 //            each u, once known, leaves all later rows' sums, so that a step waits for one
@@ -90,6 +91,8 @@ __device__ __forceinline__ uint32_t tf32_rn(float x) {
     return r;
 }
 
+__device__ __forceinline__ float round_tf32(float x) { return __uint_as_float(tf32_rn(x)); }
+
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
@@ -121,8 +124,7 @@ __device__ __forceinline__ float warp_sum8(const float (&x)[8], int lane) {
 template <bool kRound>   // to tf32, for the plain product
 __device__ __forceinline__ void store_frag(float* tile, int r, int lane, float4 x) {
     if (kRound)
-        x = make_float4(__uint_as_float(tf32_rn(x.x)), __uint_as_float(tf32_rn(x.y)),
-                        __uint_as_float(tf32_rn(x.z)), __uint_as_float(tf32_rn(x.w)));
+        x = make_float4(round_tf32(x.x), round_tf32(x.y), round_tf32(x.z), round_tf32(x.w));
     const int ks = lane >> 1, l0 = (r & 7) * 4 + 2 * (lane & 1);
     float* p = tile + ks * 128 + 2 * (r >> 3);
     *reinterpret_cast<float2*>(p + 4 * (l0 ^ (ks & 7))) = make_float2(x.x, x.y);
@@ -135,8 +137,7 @@ __device__ __forceinline__ float4 load_frag(const float* tile, int ks, int lane)
 
 // acc += one 16-row tile (fragments a) times 16 columns of the state (this lane's rows 2 t and
 // 2 t + 1 of 8, columns 2 g and 2 g + 1: one per 8-column product).
-// Without kSplit the fragments are tf32 values already, and the state's low bits, which the
-// product does not read, are cut off (2^-10 of an element at most).
+// Without kSplit both operands are tf32 values already (2^-11 of an element at most, to nearest).
 template <bool kSplit>
 __device__ __forceinline__ void mma_step(float (&c0)[4], float (&c1)[4], float4 f, float2 p,
                                          float2 q) {
@@ -427,8 +428,12 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
     steep = __syncthreads_or(steep);
     if (!steep) {
 #pragma unroll
-        for (int m = 0; m < kMine; ++m)
-            *reinterpret_cast<float4*>(sm.k + (m * kWarps + warp) * kLk + 4 * lane) = over[m];
+        for (int m = 0; m < kMine; ++m) {
+            float4 x = over[m];
+            if (sizeof(Tin) == 2)
+                x = make_float4(round_tf32(x.x), round_tf32(x.y), round_tf32(x.z), round_tf32(x.w));
+            *reinterpret_cast<float4*>(sm.k + (m * kWarps + warp) * kLk + 4 * lane) = x;
+        }
         __syncthreads();
     } else {
         direct_pairs<Tin, NB>(sm, p, n, h, warp, lane);
@@ -480,6 +485,10 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
             for (int e = 0; e < kN8; ++e) {
                 s0[e] = *reinterpret_cast<const float2*>(sm.state + at0[e] + ks * 256);
                 s1[e] = *reinterpret_cast<const float2*>(sm.state + at1[e] + ks * 256);
+                if (sizeof(Tin) == 2) {
+                    s0[e] = make_float2(round_tf32(s0[e].x), round_tf32(s0[e].y));
+                    s1[e] = make_float2(round_tf32(s1[e].x), round_tf32(s1[e].y));
+                }
             }
 #pragma unroll
             for (int b = 0; b < 2 * NB; ++b) {
