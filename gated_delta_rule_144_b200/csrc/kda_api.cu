@@ -21,6 +21,12 @@
 
 namespace {
 
+// What the kernels store is what kda_get_device_error returns.
+static_assert((int)kda::DEV_OK == KDA_OK && (int)kda::DEV_TIMEOUT == KDA_ERR_TIMEOUT &&
+                  (int)kda::DEV_BAD_SEQLENS == KDA_ERR_BAD_SEQLENS &&
+                  (int)kda::DEV_RANGE == KDA_ERR_RANGE &&
+                  (int)kda::DEV_BAD_INDEX == KDA_ERR_BAD_INDEX, "device error codes");
+
 // Sticky device error word (one per device context; see kda_get_device_error).
 __device__ unsigned g_device_error = 0;
 

@@ -15,6 +15,7 @@ enum DeviceError : unsigned {
     DEV_TIMEOUT = 4,
     DEV_BAD_SEQLENS = 5,
     DEV_RANGE = 6,   // reserved: steep decays take the chunked kernels' direct path instead
+    DEV_BAD_INDEX = 7,   // a tree parent, path row or state page out of range
 };
 
 // The first error sticks; later ones are dropped.

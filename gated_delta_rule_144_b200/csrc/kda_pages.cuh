@@ -1,11 +1,9 @@
-// Pages of a pool of states, and the device error of an index out of range (rows and parents too).
+// Pages of a pool of states.
 #pragma once
 
 #include "kda_internal.cuh"
 
 namespace kda {
-
-constexpr unsigned DEV_BAD_INDEX = 7;   // beside DeviceError's; equals KDA_ERR_BAD_INDEX
 
 // Page dst[i] <- page src[i] (-1: zeros) of pool [layers][pages][page_bytes], i < n; dst[i] = -1
 // does nothing. Conflicting or out-of-range pairs are left out and set DEV_BAD_INDEX.

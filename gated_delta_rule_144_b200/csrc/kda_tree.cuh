@@ -1,7 +1,7 @@
 // Read-outs of a tree of drafted tokens against a state, and the state advanced along a path.
 #pragma once
 
-#include "kda_pages.cuh"
+#include "kda_internal.cuh"
 
 namespace kda {
 
