@@ -1053,9 +1053,9 @@ kda_status_t kda_commit_path(int N, int H, int T, int A, kda_dtype_t dtype, cons
     kda_status_t st = check_tree_sizes(N, H, T, dtype);
     if (st != KDA_OK) return st;
     if (A < 0) return fail(KDA_ERR_INVALID_ARG, "bad sizes A=%d", A);
-    const bool any = N > 0 && T > 0 && A > 0;
-    if ((st = check_ptr(k, "k", any)) || (st = check_ptr(v, "v", any)) ||
-        (st = check_ptr(log_g, "log_g", any)) || (st = check_ptr(beta, "beta", any)) ||
+    const bool any = N > 0 && A > 0, read = any && T > 0;   // (T = 0: no path may name a row)
+    if ((st = check_ptr(k, "k", read)) || (st = check_ptr(v, "v", read)) ||
+        (st = check_ptr(log_g, "log_g", read)) || (st = check_ptr(beta, "beta", read)) ||
         (st = check_ptr(path, "path", any)) || (st = check_ptr(S_inout, "S_inout", any)))
         return st;
     if (!any) return KDA_OK;
