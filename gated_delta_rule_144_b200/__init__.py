@@ -575,6 +575,12 @@ def _empty(like, shape, dtype, stream):
         return _empty(like, shape, dtype, None)
 
 
+def _int32(*sizes):
+    """Sizes reach the library as C ints."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("sizes above 2^31 - 1 are not supported")
+
+
 def _call(fn, where, device, *args):
     """Call the library with `device` current, and check the status."""
     if torch._C._cuda_getDevice() == device.index:
@@ -609,6 +615,7 @@ def _linear_inputs(q, k, v, log_g, lead_dims):
     vs = v.shape
     if len(vs) != len(qs) or vs[:-2] != qs[:-2]:
         raise ValueError("v must be shaped like q but for its heads and head dim")
+    _int32(*qs, vs[-2], vs[-1])
     if not isinstance(log_g, torch.Tensor) or log_g.dim() != 1:
         _dev(log_g, "log_g", torch.float32, vs[:-1], dev)
         return dev, qs, vs[-2], vs[-1], GATE_TOKEN
@@ -636,6 +643,7 @@ def linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, *, output_final_state: 
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be a 1-D int32 tensor of N + 1 offsets")
         N = cu_seqlens.numel() - 1
+        _int32(N)
     state = (N, H, dk, dv)
     _dev(h0, "h0", torch.float32, state, dev)
     if o is None:
@@ -690,6 +698,7 @@ def _tree_rows(k, v, log_g, beta, S):
     if k.dim() != 4 or k.shape[3] != 128:
         raise ValueError("k must be [N, T, H, 128]")
     N, T, H, d = k.shape
+    _int32(N, T, H)
     _dtype_code(k)
     _dev(v, "v", dt, k.shape, dev)
     _dev(log_g, "log_g", torch.float32, k.shape, dev)
@@ -730,6 +739,7 @@ def commit_path(k, v, log_g, beta, path, S, *, stream=None):
     _dev(path, "path", torch.int32, None, dev)
     if path.dim() != 2 or path.shape[0] != N:
         raise ValueError("path must be [N, A]")
+    _int32(path.shape[1])
     _call(L.kda_commit_path, "kda_commit_path", dev, N, H, T, path.shape[1], _dtype_code(k),
           k.data_ptr(), v.data_ptr(), log_g.data_ptr(), beta.data_ptr(), path.data_ptr(),
           S.data_ptr(), _handle(stream, dev))
@@ -753,6 +763,7 @@ def state_copy(S, src, dst, *, page_dim: int = 0, stream=None):
     layers = 1
     for x in shape[:page_dim]:
         layers *= x
+    _int32(layers, shape[page_dim], src.numel())
     page = S.element_size()
     for x in shape[page_dim + 1:]:
         page *= x
