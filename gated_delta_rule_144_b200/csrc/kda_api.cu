@@ -806,7 +806,8 @@ static kda_status_t check_linear_desc(const kda_linear_desc_t* d, bool has_cu) {
         return fail(KDA_ERR_INVALID_ARG, "num_seqs (%d) must equal B (%d) without cu_seqlens",
                     d->num_seqs, d->B);
     }
-    if ((int64_t)d->B * d->T * d->H > (int64_t)1 << 40 || (int64_t)d->B * d->T > 0x7fffffffLL ||
+    // (a row or a segment's first one, up to T and a segment's length behind it, is held in an int)
+    if ((int64_t)d->B * d->T * d->H > (int64_t)1 << 40 || (int64_t)d->B * d->T > 1 << 30 ||
         (int64_t)d->num_seqs * d->H > 0x7fffffffLL)
         return fail(KDA_ERR_INVALID_ARG, "problem too large");
     return KDA_OK;

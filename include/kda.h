@@ -344,7 +344,8 @@ kda_status_t kda_decode_tokens(int N, int H, int T, int dk, int dv, kda_dtype_t 
  *
  *     S = exp(log_g_t) S + k_t v_t^T,     o_t = S^T q_t       (read-out after the write; no scale)
  *
- *   B, T, H, dk, dv : batch, tokens per row, value heads, key and value head dims (dk, dv <= 256).
+ *   B, T, H, dk, dv : batch, tokens per row (B * T <= 2^30), value heads, key and value head dims
+ *                     (dk, dv <= 256).
  *   Hk              : query/key heads; H % Hk == 0 and value head h reads q, k head h / (H / Hk).
  *   num_seqs, dtype : as in kda_fwd_desc_t (dtype: q, k, v and o).
  *   gate            : KDA_GATE_TOKEN: log_g is [B, T, H]; KDA_GATE_HEAD: log_g is [H], one decay
