@@ -633,7 +633,8 @@ def linear_fwd(q, k, v, log_g, h0=None, cu_seqlens=None, *, output_final_state: 
     decay per head. h0: [N, H, dk, dv] fp32 or None. cu_seqlens: int32 [N + 1] on the device (B
     must be 1) or None. Returns (o [B, T, H, dv], hT [N, H, dk, dv] fp32 or None). o, hT and the
     workspace must overlap nothing else. The workspace (uint8, linear_fwd_workspace_size bytes) is
-    allocated here when not given; calls that may overlap need one each.
+    allocated here when not given; calls that may overlap need one each. At most 2^30 tokens. No
+    gradient is recorded.
     """
     L = lib()
     dev, (B, T, Hk, dk), H, dv, gate = _linear_inputs(q, k, v, log_g, (4,))

@@ -40,10 +40,11 @@
 // outgrows the cache (132 KB of code ran a chunk in 7.2 us, the same loops rolled up, 77 KB, in
 // 3.3 us).
 // Bound: shared memory. A chunk of a CTA takes about 3690 cycles, of which about 3375 move operands,
-// decayed V, state and output through it. 2 x 65536 tokens x 32 heads x 128 x 128 take 1.08 to 1.16
-// ms in a burst (0.58 of the measured copy rate) and 1.31 to 1.36 in a long run, where the power
-// limit holds the clock down; eight packed documents of 28937 tokens, 32 heads of 64 columns 156 to
-// 165 us; one prompt of 4096 tokens x 16 heads 47 us. Not kept, on the first of these: tiles fetched
+// decayed V, state and output through it. 2 x 65536 tokens x 32 heads x 128 x 128 take 1.36 to 1.37
+// ms in a long run (0.48 of the measured copy rate), where the power limit holds the clock down, and
+// 1.08 to 1.27 in the first tens of calls; eight packed documents of 28937 tokens, 32 heads of 64
+// columns 168 us (150 as a replayed graph); one prompt of 4096 tokens x 16 heads 49 us (47). Not kept,
+// on the first of these, a few calls at a time: tiles fetched
 // into L2 two chunks ahead 1.15 (against 1.10), one product of 192 columns for all terms 1.36
 // (1.15), the last quarter of the values by the state warps 1.30 (1.15), outputs stored by each warp
 // for itself 1.23 (1.14).

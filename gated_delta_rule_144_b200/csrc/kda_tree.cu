@@ -10,29 +10,34 @@
 // node) follows the tree's order. A path's rows are a tree without branches, and the state after
 // its last row e is diag(d_e) S + sum_j (d_ej k_j) u_j^T.
 //
-// The tree: one block of 256 threads per (sequence, head), two per SM, up to 32 nodes (512 threads,
-// one per SM, above). Phases:
+// The tree: one block of 256 threads per (sequence, head) up to 32 nodes, 512 above; two blocks per SM
+// up to 16 nodes, one above (the shared memory of 17 to 32 nodes is 126 KB: 128 sequences x 32 heads
+// of 16 bf16 nodes 109 us, of 18 to 24 nodes 289). Phases:
 //   load     S by TMA into shared memory, under way until the product; the rows of k and the
 //            gates.
 //   paths    d_i of every node, one after another: a thread per channel, no barrier between them.
 //   pairs    d_ij = d_i / d_j, so all pairs are one product [k d; q d] (k / d)^T on the tensor
 //            cores, of which the tree keeps its own. Where some d is below 1e-20 (a gate of -inf
 //            included) the quotient leaves the range: then a warp per node walks the node's
-//            ancestors with d_ij in registers, where only products of gates <= 1 appear.
+//            ancestors with d_ij in registers, where only products of gates <= 1 appear. One such
+//            channel of one node sends the whole (sequence, head) there. With gates of
+//            -softplus(N(2, 1)) that is 10 % of chains of 16 nodes and nearly all of 18 or more:
+//            128 sequences x 32 heads, chains of 18 nodes 567 us against 289, one sequence's chain
+//            of 61 nodes 78 us against 18.5 of a bushy tree.
 //   product  [k d; q d] S on the tensor cores (warp-level tf32 products: 16 x 8 x 8). The tree of
-//            bf16 rows uses one tf32 product (its operands, rounded to nearest, lose at most 2^-11
-//            each, below the bf16 output's 2^-8; with S and k / d cut off instead, 2^-10 and always
-//            towards zero, 128 sequences x 32 heads of 16 nodes take 2 us less); fp32 rows split both operands into a tf32 part and a tf32
-//            remainder and sum three products (2^-21).
+//            bf16 rows uses one tf32 product: its operands, rounded to nearest, lose at most 2^-11
+//            each, below the bf16 output's 2^-8 (S and k / d cut off instead lose 2^-10, always
+//            towards zero, and save 2 of 109 us). fp32 rows split both operands into a tf32 part
+//            and a tf32 remainder and sum three products (2^-21).
 //   solve    a thread per value column and block of 16 nodes substitutes forward in registers:
 //            each u, once known, leaves all later rows' sums, so that a step waits for one
 //            product only; then the blocks behind take the block's u from shared memory, and the
 //            threads that wait add it to their read-outs.
 // Bound: the phases' latency, two blocks per SM beside each other; HBM (64 KiB of state per block) in
-// the limit. 128 sequences x 32 heads, 16 bf16 nodes: 105 us (0.54 of the measured copy rate), a
+// the limit. 128 sequences x 32 heads, 16 bf16 nodes: 109 us (0.52 of the measured copy rate), a
 // block's cycles 3400 until rows and gates are there, 950 paths, 1100 quotients and fragments, 3900
-// products (a tf32 product takes 18 to 20 cycles of a scheduler), 1300 solve, 2200 read-outs. One
-// sequence of 61 nodes and 32 heads: 16.9 us in a graph (20.3 with one block per unit). Before: read-outs
+// products (a tf32 product takes 18 to 20 cycles of a scheduler), 1300 solve, 2200 read-outs (counted
+// when it took 105). One sequence of 61 nodes and 32 heads: 18.5 us. Before: read-outs
 // within the substitution and v loaded by the solve's threads 136 and 26.6 us; path products in
 // rounds that double the stretch covered 125 and 22.
 
@@ -648,9 +653,9 @@ decode_tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constan
 // k d S, the substitution for u in registers, and S = d_e S + sum_j (d_ej k_j) u_j^T, each one pass
 // over the registers. (Tensor-core products of 16-row tiles, split for fp32, take more instructions
 // up to about 9 rows: 567 us against 280 then.) Bound: HBM (the state read and written). 256
-// sequences x 32 heads, paths of up to 6 of 16 bf16 rows: 192 us, 0.89 of the measured copy
-// rate; 211 with only four rows brought ahead, 280 without the loader warp; 199 with a path's last
-// one or two rows taken as two instead of four.
+// sequences x 32 heads, paths of up to 6 of 16 bf16 rows: 192 to 202 us, 0.85 to 0.89 of the measured
+// copy rate; when it was built 192, 211 with only four rows brought ahead, 280 without the loader
+// warp; 199 with a path's last one or two rows taken as two instead of four.
 constexpr int kRows = 4;
 constexpr int kStaged = 8;   // rows of a path that the loader brings
 constexpr int kPathWorkers = 128, kPathThreads = kPathWorkers + 32;
@@ -768,9 +773,6 @@ commit_path_kernel(const TreeParams p, const int units) {
     const int phase = lane >> 3, col = 32 * warp + 4 * (lane & 7);
     for (int it = 0;; ++it) {
         const int b = it & 1;
-        // one warp waits for all, so that they go on together or not at all (and all are done with
-        // the rows before these); the others' own look at the barrier orders the copies before
-        // their reads
         // the loader arrives within two of its own bounds, whether the copies landed or not, so
         // that the four warps always take the same way here (the look at `full` orders the copies
         // before this thread's reads)

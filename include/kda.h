@@ -370,7 +370,13 @@ typedef struct {
  *   workspace  : kda_linear_fwd_workspace_size(desc) bytes, 16-byte aligned (NULL when 0): the
  *                states between the segments that long sequences are cut into, and their decays.
  * Calls that may run at the same time need a workspace each. Tokens of one document never reach
- * another's outputs, nor a token those before it, whatever values (infinities, NaN) they hold.
+ * another's outputs, nor a token those before it, whatever values (infinities, NaN) they hold; what
+ * such a value does reach is not finite, and may be NaN where the recurrence gives an infinity.
+ * Final states keep fp32 accuracy (about 1e-6 relative, bf16 inputs too). bf16 outputs of prompts on the
+ * tensor cores (dk <= 128, dk and dv multiples of 8) round the decayed products of queries and keys,
+ * and the state that a chunk of 128 tokens starts from, to bf16 before their last product: about
+ * 2.4e-3 relative in all, where the rounding of the output alone is 1.7e-3. All else is fp32 up to
+ * the output's rounding.
  */
 kda_status_t kda_linear_fwd(const kda_linear_desc_t* desc, const void* q, const void* k,
                             const void* v, const float* log_g, const float* h0,
@@ -406,8 +412,8 @@ kda_status_t kda_linear_decode(int N, int T, int H, int Hk, int dk, int dv, kda_
  *   clear_absent : 0: rows of o without a node stay as they are; else they become zero.
  * T <= KDA_TREE_MAX_NODES (KDA_ERR_UNSUPPORTED above). o must not overlap any other argument. A
  * sequence with other parents has no nodes and sets KDA_ERR_BAD_INDEX in the device error word.
- * The states meet bf16 rows in tf32 products (relative error 2^-11 per factor, below the output's
- * rounding), fp32 rows in split products (2^-21).
+ * The states meet bf16 rows in tf32 products (both factors rounded to nearest, 2^-11 relative each,
+ * below the output's rounding), fp32 rows in split products (2^-21).
  */
 #define KDA_TREE_MAX_NODES 64
 kda_status_t kda_decode_tree(int N, int H, int T, kda_dtype_t dtype, const void* q, const void* k,
@@ -436,7 +442,8 @@ kda_status_t kda_commit_path(int N, int H, int T, int A, kda_dtype_t dtype, cons
  *   src, dst : int32 [n], device
  * The copies happen in no order: a page may be read by several pairs, but no page may be written
  * twice, or both read and written. Pairs in such a conflict, or out of range, are left out and
- * set KDA_ERR_BAD_INDEX in the device error word.
+ * set KDA_ERR_BAD_INDEX in the device error word. (A page copied onto itself, and in no other pair,
+ * stays as it is without an error.)
  */
 kda_status_t kda_state_copy(void* pool, int layers, int pages, long long page_bytes,
                             const int32_t* src, const int32_t* dst, int n, kda_stream_t stream);
